@@ -254,6 +254,69 @@ MOE_API int moe_forward_w4(moe_handle h, int64_t T, const void* x, const float* 
                            size_t workspace_bytes, const moe_debug* dbg, void* stream);
 
 /*
+ * 8-bit floating point with block scales.  A matrix [rows][K] is held as e4m3
+ * codes (1 sign, 4 exponent, 3 mantissa bits, largest value 448, no infinity)
+ * and fp32 scales, one for each 128 consecutive elements of a row
+ * (block_rows 1: scales [rows][ceil(K / 128)]) or one for each 128 x 128 block
+ * (block_rows 128: scales [ceil(rows / 128)][ceil(K / 128)]); the last block
+ * of a row or column may be shorter.  Element (r, k) stands for
+ * code[r][k] * scale[r / block_rows][k / 128].
+ *
+ * moe_quantize_fp8: codes and scales of `matrices` matrices x [rows][K] (fp32
+ * or bf16, rows ld elements apart, matrices rows * ld apart).  For a block
+ * with largest magnitude m: a = max(m, 2^-100), scale = a / 448, code = e4m3(x
+ * * (448 / a)), every operation rounded to fp32 and the code to the nearest
+ * (ties to even).  With transpose != 0 the codes and scales are those of the
+ * transposed matrices [K][rows] (blocks run along the rows of x).  Codes:
+ * rows ld_codes bytes apart, matrices (rows or K) * ld_codes apart; scales
+ * contiguous.  A NaN gets the NaN code; a block that holds an infinity reads
+ * back as NaN.  Codes past the end of a row (ld_codes > its length) are left
+ * as they were.  Asynchronous on `stream`; empty matrices write nothing.
+ *
+ * moe_matmul_fp8: out[r][n] = sum_k a(r, k) b_g(n, k) for the rows r of group
+ * g, offsets[g] <= r < offsets[g + 1] (int32 on the device, ascending, [groups
+ * + 1]; NULL with one group: every row).  A [M][K] has block_rows 1; B
+ * [groups][N][K] has block_rows b_rows = 128 (weights) or 1.  out is bf16 or
+ * fp32, rows ld_out elements apart; rows of no group are left as they were.
+ * Each block of 128 along K is summed on the tensor cores, the blocks in fp32
+ * in order (the result does not depend on other rows or on timing), and the
+ * sum is rounded once.  With the quantiser's transposed form these are the
+ * three products of a linear layer y = x W^T:
+ *     y  = (x block_rows 1) (W block_rows 128)
+ *     dx = (dy block_rows 1) (W transposed, block_rows 128)
+ *     dW = (dy transposed, block_rows 1) (x transposed, block_rows 1), b_rows 1
+ *   Codes 16-byte aligned, lda and ldb multiples of 16; scales contiguous and
+ *   4-byte aligned; 1 <= groups <= 256; M may be 0, N and K at least 1.  The
+ *   product of two scales must be a normal fp32 number.  Offsets outside [0,
+ *   M] or not ascending give wrong rows, never an access outside the buffers.
+ *   workspace: moe_matmul_fp8_workspace_bytes(M, N, K, groups) bytes (may be
+ *   0), 256-byte aligned.
+ *
+ * moe_forward_fp8: moe_forward of a bf16 layer (d and d_ff multiples of 16)
+ * whose expert weights are given in that format, block_rows 128, contiguous:
+ * W1 / W3 [E (+ n_shared)][d_ff][d], W2 [E (+ n_shared)][d][d_ff].  Routing
+ * reads x itself; the experts read x and the hidden activation quantised with
+ * block_rows 1.  Arguments, results and errors as moe_forward; W3_codes and
+ * W3_scales are NULL for ReLU layers; the workspace is
+ * moe_workspace_bytes_fp8(h, T) bytes.  moe_backward does not serve layers run
+ * this way.
+ */
+MOE_API int moe_quantize_fp8(const void* x, int dtype, int64_t matrices, int64_t rows, int64_t K, int64_t ld,
+                             int block_rows, int transpose, void* codes, int64_t ld_codes, float* scales,
+                             void* stream);
+MOE_API size_t moe_matmul_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t groups);
+MOE_API int moe_matmul_fp8(int64_t M, int64_t N, int64_t K, int64_t groups, const void* a_codes, int64_t lda,
+                           const float* a_scales, const void* b_codes, int64_t ldb, const float* b_scales, int b_rows,
+                           const int32_t* offsets, void* out, int out_dtype, int64_t ld_out, void* workspace,
+                           size_t workspace_bytes, void* stream);
+MOE_API size_t moe_workspace_bytes_fp8(moe_handle h, int64_t T);
+MOE_API int moe_forward_fp8(moe_handle h, int64_t T, const void* x, const float* W_r, const float* b_r,
+                            const void* W1_codes, const float* W1_scales, const void* W3_codes,
+                            const float* W3_scales, const void* W2_codes, const float* W2_scales, void* y,
+                            int32_t* expert_counts, int32_t* dropped, float* aux_loss, float* z_loss, void* workspace,
+                            size_t workspace_bytes, const moe_debug* dbg, void* stream);
+
+/*
  * The alternative load-balancing statistics of the last moe_forward that used
  * `workspace` with T tokens (stream-ordered on `stream`), unscaled, written as
  * three fp32 values to the device pointer `out`:

@@ -1,0 +1,578 @@
+// Grouped product of two e4m3 operands with block scales on the 5th-generation
+// tensor cores (tcgen05 + TMEM), fed by TMA:
+//
+//   y[r][n] = sum_kb sa[r][kb] sb[n or n / 128][kb] sum_{k in block kb} A[r][k] B_g[n][k]
+//
+// for the rows r of every group g (offsets on the device; one group without
+// them).  The scales are arbitrary fp32 numbers, so the tensor core sums one
+// k-block of 128 (one 128-byte swizzled row of shared memory, four MMAs of
+// K = 32) into its own TMEM accumulator, and the epilogue warps read it back,
+// multiply by sa * sb and add it to fp32 registers while the next k-block's
+// MMAs fill the other accumulator.  Tiles are 128 rows x 256 columns: a
+// k-block's MMAs take 512 cycles at the tensor cores' rate, its read-back and
+// promotion 128 columns for each of the eight epilogue warps.
+//
+// Warp roles (320 threads, one CTA per SM):
+//   warp 0       TMA producer
+//   warp 1       TMEM allocator; lane 0 issues tcgen05.mma
+//   warps 2..9   promotion and epilogue: warp w owns TMEM lanes 32 (w % 4) ..
+//                (rows of the tile) and the columns of half (w - 2) / 4
+// Pipelines: a ring of shared-memory stages (full / empty) and two TMEM
+// accumulators of 256 columns (tfull / tempty), one k-block each.  Every wait
+// is bounded; one that runs out records MOE_ERR_TIMEOUT, raises the CTA's
+// abort flag, and the CTA drains its copies and MMAs, frees TMEM and returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "fp8.cuh"
+#include "fp8.h"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int BM = 128;
+constexpr int BK = 128;                 // e4m3 elements per 128-byte shared-memory row
+constexpr int MMA_N = 256;
+constexpr int B_HALF = 128 * BK;        // 16 KB per 128 rows of B
+constexpr int MAX_STAGES = 6;
+constexpr int NUM_THREADS = 320;
+constexpr int EPI_WARPS = 8;
+constexpr uint32_t TMEM_COLS = 2 * MMA_N;
+constexpr int ROW_STAGE = 80;           // bytes per staged output row: 64 + 16 of padding
+
+// AR: rows of A a stage holds.  No group has more rows than max_group_rows, so
+// a small batch stages 32 or 64 and keeps more weight bytes in flight; the
+// M = 128 MMA then reads the bytes that follow, which only feed accumulator
+// rows that are never stored.
+template <int AR>
+struct Geo {
+  static constexpr int A_ST = AR * BK;
+  static constexpr int STAGE_BYTES = A_ST + 2 * B_HALF;
+  static constexpr int STAGES = (196 * 1024 / STAGE_BYTES) < MAX_STAGES ? (196 * 1024 / STAGE_BYTES) : MAX_STAGES;
+};
+
+struct Ctl {
+  uint64_t full[MAX_STAGES];
+  uint64_t empty[MAX_STAGES];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint64_t drain;
+  uint32_t tmem_slot;
+  volatile int abort;
+  int mprefix[kFp8MaxGroups + 1];
+  int offsets[kFp8MaxGroups + 1];
+  float hmax[2][BM];
+  alignas(16) float sb[2][2][128];      // per-row scales of B: [column half][parity][column]
+  alignas(16) uint8_t stage_out[EPI_WARPS][32 * ROW_STAGE];
+};
+
+template <int AR>
+constexpr size_t smem_bytes() {
+  return Geo<AR>::STAGES * Geo<AR>::STAGE_BYTES + sizeof(Ctl) + 1024;
+}
+
+// kind::f8f6f4: e4m3 A and B (format fields 0, both K-major), fp32 D.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Group tables from the caller's offsets, clamped into [0, rows] and made
+// ascending by a running maximum (a bad table can give wrong rows, never an
+// access outside the buffers): offsets and the running count of 128-row tiles.
+// One warp; lane l takes groups 8 l .. 8 l + 7.
+__device__ __forceinline__ void load_groups(Ctl* c, const Fp8Params& p, int lane) {
+  static_assert(kFp8MaxGroups == 256, "eight groups per lane");
+  const int rows = static_cast<int>(p.a_rows);
+  if (p.offsets == nullptr) {
+    if (lane == 0) {
+      c->offsets[0] = 0;
+      c->offsets[1] = rows;
+      c->mprefix[0] = 0;
+      c->mprefix[1] = (rows + BM - 1) / BM;
+    }
+    return;
+  }
+  const int first = min(max(p.offsets[0], 0), rows);
+  int end[8];  // offsets[g + 1]
+  int run = first;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int g = lane * 8 + i;
+    const int o = g < p.G ? min(max(p.offsets[g + 1], 0), rows) : 0;
+    run = max(run, o);
+    end[i] = run;
+  }
+  int before = run;  // running maximum over the lanes below
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before = max(before, v);
+  }
+  before = __shfl_up_sync(0xffffffffu, before, 1);
+  if (lane == 0) before = first;
+  int tiles = 0, prev = before;
+  int cum[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    end[i] = max(end[i], before);
+    tiles += (end[i] - prev + BM - 1) / BM;
+    prev = end[i];
+    cum[i] = tiles;
+  }
+  int sum = tiles;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += v;
+  }
+  const int base = sum - tiles;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int g = lane * 8 + i;
+    if (g < p.G) {
+      c->offsets[g + 1] = end[i];
+      c->mprefix[g + 1] = base + cum[i];
+    }
+  }
+  if (lane == 0) {
+    c->offsets[0] = first;
+    c->mprefix[0] = 0;
+  }
+}
+
+// Unit u of the work: tile u / ksplit (group-major, then column tile, then row
+// tile, so that tiles sharing B run together), K range u % ksplit.
+struct Item {
+  int g, mt, nt, ks, kb0, kb1;
+};
+__device__ __forceinline__ bool item_at(const Ctl* c, const Fp8Params& p, int64_t u, Item& w) {
+  if (u >= static_cast<int64_t>(c->mprefix[p.G]) * p.n_tiles * p.ksplit) return false;
+  const int t = static_cast<int>(u / p.ksplit);
+  w.ks = static_cast<int>(u - static_cast<int64_t>(t) * p.ksplit);
+  int lo = 0, hi = p.G;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (c->mprefix[mid] * p.n_tiles <= t) lo = mid; else hi = mid;
+  }
+  w.g = lo;
+  const int local = t - c->mprefix[lo] * p.n_tiles;
+  const int mtiles = c->mprefix[lo + 1] - c->mprefix[lo];
+  w.nt = local / mtiles;
+  w.mt = local - w.nt * mtiles;
+  w.kb0 = w.ks * p.kb_per;
+  w.kb1 = min(p.num_kb, w.kb0 + p.kb_per);
+  return true;
+}
+
+__device__ __forceinline__ float silu_mul(float a, float b) { return __fdividef(a, 1.f + __expf(-a)) * b; }
+
+template <int EPI, int AR, bool SB1>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
+                    const __grid_constant__ CUtensorMap tmB1, const Fp8Params p) {
+  constexpr bool PAIR = EPI == FP8_SWIGLU;  // 128 columns of W1 and the same of W3
+  constexpr bool ACT = EPI == FP8_SWIGLU || EPI == FP8_RELU;
+  constexpr uint32_t IDESC = idesc_e4m3_f32(BM, MMA_N);
+  using G = Geo<AR>;
+  constexpr int STAGES = G::STAGES, STAGE_BYTES = G::STAGE_BYTES, A_ST = G::A_ST;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stages = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Ctl* ctl = reinterpret_cast<Ctl*>(stages + STAGES * STAGE_BYTES);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) { mbar_init(&ctl->full[s], 1); mbar_init(&ctl->empty[s], 1); }
+    for (int a = 0; a < 2; ++a) { mbar_init(&ctl->tfull[a], 1); mbar_init(&ctl->tempty[a], EPI_WARPS); }
+    mbar_init(&ctl->drain, 1);
+    ctl->abort = 0;
+    fence_mbarrier_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB0);
+    if (PAIR) tma_prefetch_desc(&tmB1);
+  }
+  if (warp == 1) tmem_alloc(&ctl->tmem_slot, TMEM_COLS);
+  pdl_wait();  // the operands and the group table come from the kernels before
+  pdl_trigger();
+  if (warp == 2) load_groups(ctl, p, lane);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = ctl->tmem_slot;
+  Item w;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, issued_phase = 0;
+      bool ok = true;
+      for (int64_t u = blockIdx.x; ok && item_at(ctl, p, u, w); u += gridDim.x) {
+        const int row0 = ctl->offsets[w.g] + w.mt * BM;
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (!mbar_wait_or_abort(&ctl->empty[stage], phase ^ 1u, &ctl->abort, p.err, p.limit_ns)) { ok = false; break; }
+          uint8_t* sa = stages + stage * STAGE_BYTES;
+          mbar_arrive_expect_tx(&ctl->full[stage], A_ST + 2 * B_HALF);
+          tma_load_2d(sa, &tmA, &ctl->full[stage], kb * BK, row0);
+          if (PAIR) {
+            tma_load_3d(sa + A_ST, &tmB0, &ctl->full[stage], kb * BK, w.nt * 128, w.g);
+            tma_load_3d(sa + A_ST + B_HALF, &tmB1, &ctl->full[stage], kb * BK, w.nt * 128, w.g);
+          } else {
+            tma_load_3d(sa + A_ST, &tmB0, &ctl->full[stage], kb * BK, w.nt * 256, w.g);  // 256-row box
+          }
+          issued |= 1u << stage;
+          issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      // Drain: every issued copy must have landed before the CTA may exit.
+      for (int s = 0; s < STAGES; ++s)
+        if ((issued >> s) & 1u) mbar_wait(&ctl->full[s], (issued_phase >> s) & 1u, p.limit_ns);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int64_t u = blockIdx.x; ok && item_at(ctl, p, u, w); u += gridDim.x) {
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (!mbar_wait_or_abort(&ctl->tempty[acc], acc_phase ^ 1u, &ctl->abort, p.err, p.limit_ns) ||
+              !mbar_wait_or_abort(&ctl->full[stage], phase, &ctl->abort, p.err, p.limit_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(stages + stage * STAGE_BYTES);
+          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * MMA_N);
+#pragma unroll
+          for (int k = 0; k < BK / 32; ++k)
+            umma_f8(d_tmem, sdesc_k_sw128(sa + k * 32), sdesc_k_sw128(sa + A_ST + k * 32), IDESC, k != 0 ? 1u : 0u);
+          umma_commit(&ctl->empty[stage]);
+          umma_commit(&ctl->tfull[acc]);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+        }
+      }
+      // Drain: all MMAs of this CTA complete before TMEM is freed.
+      umma_commit(&ctl->drain);
+      mbar_wait(&ctl->drain, 0, p.limit_ns);
+    }
+  } else {
+    // ------------------------------------------------------------ promotion and epilogue
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const int r_in_tile = q * 32 + lane;
+    uint8_t* stg = ctl->stage_out[warp - 2];
+    // PAIR: columns [64 half, +64) of W1, then of W3; else columns [128 half, +128)
+    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    const uint32_t col0 = PAIR ? 64u * half : 128u * half, col2 = PAIR ? 128u + 64u * half : 128u * half + 64u;
+    int acc_i = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; ok && item_at(ctl, p, u, w); u += gridDim.x) {
+      const int m_local = w.mt * BM + r_in_tile;
+      const int row = ctl->offsets[w.g] + m_local;
+      const bool vrow = row < ctl->offsets[w.g + 1];
+      const bool warp_live = __any_sync(0xffffffffu, vrow);
+      // scales: this row's of A, and of B's 128-row block(s)
+      const int bn_blocks = (p.N + 127) >> 7;
+      const int nb = PAIR ? w.nt : min(2 * w.nt + half, bn_blocks - 1);
+      const float* sa = p.sa + (vrow ? static_cast<int64_t>(row) : 0) * p.sa_ld;
+      const float* sb0 = p.sb0 + w.g * p.sb_gs + (SB1 ? 0 : static_cast<int64_t>(nb) * p.num_kb);
+      const float* sb1 = PAIR ? p.sb1 + w.g * p.sb_gs + static_cast<int64_t>(nb) * p.num_kb : nullptr;
+      const int my_n = w.nt * 256 + half * 128 + (threadIdx.x - 64 - half * 128);  // SB1: the column this thread fetches
+      float acc[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+#pragma unroll 1
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        const float s_a = vrow ? __ldg(sa + kb) : 0.f;
+        const float s0 = SB1 ? s_a : s_a * __ldg(sb0 + kb);
+        const float s1 = PAIR ? s_a * __ldg(sb1 + kb) : s0;
+        float* sbs = ctl->sb[half][acc_i];  // (turns with the accumulator: the last block's may still be read)
+        if (SB1) {  // this half's 128 scales of B, one per thread
+          sbs[threadIdx.x - 64 - half * 128] = my_n < p.N ? __ldg(sb0 + static_cast<int64_t>(my_n) * p.num_kb + kb) : 0.f;
+          named_barrier(1 + half, 128);
+        }
+        ok = ok && __all_sync(0xffffffffu,
+                              mbar_wait_or_abort(&ctl->tfull[acc_i], acc_phase, &ctl->abort, p.err, p.limit_ns));
+        if (ok) {
+          tc_fence_after();
+          if (warp_live) {
+            const uint32_t tb = lane_base + static_cast<uint32_t>(acc_i * MMA_N);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t t[32];
+              tmem_ld32(tb + (c < 2 ? col0 + c * 32 : col2 + (c - 2) * 32), t);
+              tmem_ld_wait();
+              if (SB1) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                  const float4 b = *reinterpret_cast<const float4*>(sbs + c * 32 + i);
+                  acc[c * 32 + i] = fmaf(__uint_as_float(t[i]), s0 * b.x, acc[c * 32 + i]);
+                  acc[c * 32 + i + 1] = fmaf(__uint_as_float(t[i + 1]), s0 * b.y, acc[c * 32 + i + 1]);
+                  acc[c * 32 + i + 2] = fmaf(__uint_as_float(t[i + 2]), s0 * b.z, acc[c * 32 + i + 2]);
+                  acc[c * 32 + i + 3] = fmaf(__uint_as_float(t[i + 3]), s0 * b.w, acc[c * 32 + i + 3]);
+                }
+              } else {
+                const float s = c < 2 ? s0 : s1;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(__uint_as_float(t[i]), s, acc[c * 32 + i]);
+              }
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->tempty[acc_i]);
+        }
+        if (++acc_i == 2) { acc_i = 0; acc_phase ^= 1u; }
+        if (!ok && !SB1) break;
+      }
+      // Where warps meet at barriers, they leave an aborted CTA together.
+      if (SB1) ok = named_barrier_and(1 + half, 128, ok);
+      if (PAIR) ok = named_barrier_and(3, 256, ok);  // (the last tile's hmax has been read, too)
+      if (ACT) {
+        // activation, then codes with one scale for each 128 columns of a row
+        constexpr int NV = PAIR ? 64 : 128;
+        const int n0 = PAIR ? w.nt * 128 + half * 64 : w.nt * 256 + half * 128;
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          acc[i] = PAIR ? silu_mul(acc[i], acc[(i + 64) & 127]) : fmaxf(acc[i], 0.f);
+          m = fmaxf(m, n0 + i < p.N ? fabsf(acc[i]) : 0.f);
+        }
+        if (PAIR) {  // the row's other 64 columns are with the other half's thread
+          ctl->hmax[half][r_in_tile] = m;
+          named_barrier(3, 256);
+          m = fmaxf(m, ctl->hmax[half ^ 1][r_in_tile]);
+        }
+        const Fp8Scale s = fp8_scale(m);
+        if (ok && vrow && n0 < p.N) {
+          uint8_t* dst = static_cast<uint8_t*>(p.out) + static_cast<int64_t>(row) * p.ld_out + n0;
+#pragma unroll
+          for (int i = 0; i < NV; i += 16) {
+            if (n0 + i < p.N)  // N is a multiple of 16
+              *reinterpret_cast<uint4*>(dst + i) = make_uint4(
+                  e4m3x4(acc[i] * s.inv, acc[i + 1] * s.inv, acc[i + 2] * s.inv, acc[i + 3] * s.inv),
+                  e4m3x4(acc[i + 4] * s.inv, acc[i + 5] * s.inv, acc[i + 6] * s.inv, acc[i + 7] * s.inv),
+                  e4m3x4(acc[i + 8] * s.inv, acc[i + 9] * s.inv, acc[i + 10] * s.inv, acc[i + 11] * s.inv),
+                  e4m3x4(acc[i + 12] * s.inv, acc[i + 13] * s.inv, acc[i + 14] * s.inv, acc[i + 15] * s.inv));
+          }
+          if (!PAIR || half == 0) p.out_scales[static_cast<int64_t>(row) * bn_blocks + (n0 >> 7)] = s.scale;
+        }
+      } else if (ok && warp_live) {
+        // 64 bytes of every row at a time through shared memory, so that the
+        // stores run along rows
+        constexpr int ELT = EPI == FP8_BF16 ? 2 : 4, PER = 64 / ELT;
+        const float g = (EPI == FP8_F32 && p.row_gate != nullptr && vrow) ? p.row_gate[row] : 1.f;
+        const int n0 = w.nt * 256 + half * 128;
+        const int nrows = min(32, ctl->offsets[w.g + 1] - (ctl->offsets[w.g] + w.mt * BM + q * 32));
+        const int64_t row_base = ctl->offsets[w.g] + w.mt * BM + q * 32;
+        uint8_t* out = static_cast<uint8_t*>(p.out) + static_cast<int64_t>(w.ks) * p.split_stride * ELT;
+#pragma unroll
+        for (int c = 0; c < 128 / PER; ++c) {
+          uint4* srow = reinterpret_cast<uint4*>(stg + lane * ROW_STAGE);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            if (EPI == FP8_BF16) {
+              const float* s = acc + c * PER + v * 8;
+              srow[v] = make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]),
+                                   pack_bf16x2(s[6], s[7]));
+            } else {
+              const float* s = acc + c * PER + v * 4;
+              srow[v] = make_uint4(__float_as_uint(s[0] * g), __float_as_uint(s[1] * g), __float_as_uint(s[2] * g),
+                                   __float_as_uint(s[3] * g));
+            }
+          }
+          __syncwarp();
+          const int col = n0 + c * PER;
+          if (p.vec_out) {
+            const int seg = lane & 3;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int rr = (lane >> 2) + 8 * i;
+              if (rr < nrows && col + seg * (16 / ELT) < p.N)
+                *reinterpret_cast<uint4*>(out + ((row_base + rr) * p.ld_out + col) * ELT + seg * 16) =
+                    *reinterpret_cast<const uint4*>(stg + rr * ROW_STAGE + seg * 16);
+            }
+          } else {
+#pragma unroll 1
+            for (int i = lane; i < 32 * PER; i += 32) {
+              const int rr = i / PER, cc = i % PER;
+              if (rr < nrows && col + cc < p.N) {
+                if (EPI == FP8_BF16)
+                  *reinterpret_cast<uint16_t*>(out + ((row_base + rr) * p.ld_out + col + cc) * ELT) =
+                      *reinterpret_cast<const uint16_t*>(stg + rr * ROW_STAGE + cc * 2);
+                else
+                  *reinterpret_cast<float*>(out + ((row_base + rr) * p.ld_out + col + cc) * ELT) =
+                      *reinterpret_cast<const float*>(stg + rr * ROW_STAGE + cc * 4);
+              }
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------- partials
+template <bool BF16>
+__global__ void __launch_bounds__(256) fp8_reduce_kernel(const Fp8ReduceArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  int64_t r0 = 0, r1 = a.rows;
+  if (a.offsets != nullptr) {  // as the product's kernel takes them: clamped, ascending
+    __shared__ int s_last;
+    if (threadIdx.x == 0) s_last = 0;
+    __syncthreads();
+    for (int g = threadIdx.x; g <= a.G; g += blockDim.x)
+      atomicMax(&s_last, min(max(a.offsets[g], 0), static_cast<int>(a.rows)));
+    __syncthreads();
+    r0 = min(max(a.offsets[0], 0), static_cast<int>(a.rows));
+    r1 = s_last;
+  }
+  const int64_t n = (r1 - r0) * a.N, base = r0 * a.N;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    float v = 0.f;
+    for (int k = 0; k < a.ksplit; ++k) v += a.P[k * a.split_stride + base + i];
+    const int64_t r = (base + i) / a.N, c = (base + i) - r * a.N;
+    if (BF16) static_cast<__nv_bfloat16*>(a.out)[r * a.ld_out + c] = __float2bfloat16(v);
+    else static_cast<float*>(a.out)[r * a.ld_out + c] = v;
+  }
+}
+
+// ---------------------------------------------------------------- host
+bool map_3d(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint64_t mats, uint64_t ld, uint64_t gs,
+            uint32_t box_rows) {
+  const uint64_t dims[3] = {K, rows, mats};
+  const uint64_t strides[2] = {ld, gs};
+  const uint32_t box[3] = {static_cast<uint32_t>(BK), box_rows, 1};
+  return make_map_u8(m, base, 3, dims, strides, box);
+}
+
+template <int EPI, int AR, bool SB1>
+cudaError_t launch_t(const Fp8Plan& pl, int num_sms, cudaStream_t s) {
+  constexpr size_t bytes = smem_bytes<AR>();
+  static_assert(bytes <= 227 * 1024, "8-bit product: shared memory");
+  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(&fp8_gemm_kernel<EPI, AR, SB1>),
+                                      static_cast<int>(bytes));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(fp8_gemm_kernel<EPI, AR, SB1>, dim3(num_sms), dim3(NUM_THREADS), bytes, s, pl.a, pl.b0, pl.b1, pl.p);
+}
+
+template <int EPI>
+cudaError_t launch_ar(const Fp8Plan& pl, int num_sms, cudaStream_t s) {
+  if constexpr (EPI == FP8_BF16 || EPI == FP8_F32)
+    if (pl.sb1) return launch_t<EPI, 128, true>(pl, num_sms, s);
+  if (pl.ar == 32) return launch_t<EPI, 32, false>(pl, num_sms, s);
+  if (pl.ar == 64) return launch_t<EPI, 64, false>(pl, num_sms, s);
+  return launch_t<EPI, 128, false>(pl, num_sms, s);
+}
+
+}  // namespace
+
+int fp8_ksplit(int64_t rows, int G, int N, int K) {
+  // Most 128-row tiles `rows` rows can make over G groups.
+  const int64_t g = std::min<int64_t>(G, rows);
+  const int64_t tiles = (g + (rows - g) / BM) * ((N + 255) / 256);
+  const int64_t num_kb = (K + BK - 1) / BK;
+  if (tiles <= 0 || tiles > 4 * kSplitTargetCtas) return 1;
+  // The cut whose longest CTA (ceil(units / SMs) ranges of `per` k-blocks) is
+  // shortest; more ranges only for a gain above 3 % (each adds fp32 partials).
+  int64_t best = 1, best_len = (tiles + kSplitTargetCtas - 1) / kSplitTargetCtas * num_kb;
+  for (int64_t ks = 2; ks <= num_kb / 2; ++ks) {
+    const int64_t per = (num_kb + ks - 1) / ks;
+    const int64_t ranges = (num_kb + per - 1) / per;
+    const int64_t len = (tiles * ranges + kSplitTargetCtas - 1) / kSplitTargetCtas * per;
+    if (len * 32 < best_len * 31) { best = ranges; best_len = len; }
+  }
+  return static_cast<int>(best);
+}
+
+cudaError_t plan_fp8(const Fp8Args& g, Fp8Plan* pl, const char** why) {
+  *why = nullptr;
+  const bool pair = g.epi == FP8_SWIGLU;
+  pl->epi = g.epi;
+  pl->sb1 = g.b_rows == 1;
+  pl->ar = pl->sb1 ? 128 : g.max_group_rows <= 32 ? 32 : g.max_group_rows <= 64 ? 64 : 128;
+  const uint64_t ad[2] = {static_cast<uint64_t>(g.K), static_cast<uint64_t>(g.a_rows)};
+  const uint64_t as[1] = {static_cast<uint64_t>(g.lda)};
+  const uint32_t abox[2] = {static_cast<uint32_t>(BK), static_cast<uint32_t>(pl->ar)};
+  const uint64_t K = g.K, N = g.N, G = g.G, ldb = g.ldb, gsb = g.gsb;
+  if (!make_map_u8(&pl->a, g.A, 2, ad, as, abox) || !map_3d(&pl->b0, g.B0, K, N, G, ldb, gsb, pair ? 128 : 256) ||
+      !map_3d(&pl->b1, pair ? g.B1 : g.B0, K, N, G, ldb, gsb, 128)) {
+    *why = "cuTensorMapEncodeTiled failed (alignment or driver entry point)";
+    return cudaErrorInvalidValue;
+  }
+  Fp8Params& p = pl->p;
+  p.G = g.G;
+  p.N = g.N;
+  p.K = g.K;
+  p.bn = pair ? 128 : 256;
+  p.n_tiles = (g.N + p.bn - 1) / p.bn;
+  p.num_kb = (g.K + BK - 1) / BK;
+  p.ksplit = g.epi == FP8_F32 ? std::max(1, std::min(g.ksplit, p.num_kb)) : 1;
+  p.kb_per = (p.num_kb + p.ksplit - 1) / p.ksplit;
+  p.a_rows = g.a_rows;
+  p.sa = g.sa;
+  p.sa_ld = g.sa_ld;
+  p.sb0 = g.sb0;
+  p.sb1 = g.sb1;
+  p.sb_gs = static_cast<int64_t>(pl->sb1 ? g.N : (g.N + 127) / 128) * p.num_kb;
+  p.out = g.out;
+  p.ld_out = g.ld_out;
+  p.split_stride = g.split_stride;
+  p.out_scales = g.out_scales;
+  const int elt = g.epi == FP8_BF16 ? 2 : 4;
+  p.vec_out = ((reinterpret_cast<uintptr_t>(g.out) | static_cast<uintptr_t>(g.ld_out * elt) |
+                static_cast<uintptr_t>(static_cast<int64_t>(g.N) * elt) | static_cast<uintptr_t>(g.split_stride * elt)) & 15) == 0;
+  p.row_gate = g.row_gate;
+  p.offsets = g.offsets;
+  p.err = g.err;
+  p.limit_ns = kWaitLimitNs;
+  return cudaSuccess;
+}
+
+cudaError_t launch_fp8(const Fp8Plan& pl, int num_sms, cudaStream_t s) {
+  switch (pl.epi) {
+    case FP8_BF16: return launch_ar<FP8_BF16>(pl, num_sms, s);
+    case FP8_F32: return launch_ar<FP8_F32>(pl, num_sms, s);
+    case FP8_SWIGLU: return launch_ar<FP8_SWIGLU>(pl, num_sms, s);
+    default: return launch_ar<FP8_RELU>(pl, num_sms, s);
+  }
+}
+
+cudaError_t launch_fp8_reduce(const Fp8ReduceArgs& a, cudaStream_t s) {
+  const int64_t n = a.rows * a.N;
+  if (n <= 0) return cudaSuccess;
+  const int64_t blocks = std::min<int64_t>((n + 255) / 256, 148 * 8);
+  if (a.out_is_bf16) return launch_pdl(fp8_reduce_kernel<true>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a);
+  return launch_pdl(fp8_reduce_kernel<false>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a);
+}
+
+}  // namespace moe

@@ -21,6 +21,8 @@ struct RoutingArgs {
   int nblk;          // ceil(T / kRouterTokens)
   int x_is_bf16;
   const void* x;
+  const void* x_rows;  // the rows the dispatch copies: x, or its 8-bit image (codes and scales)
+  int d_rows;          // elements (of x's type) in one of them
   const float* W_r;
   const float* b_r;
   const float* logits_in;
@@ -42,7 +44,7 @@ struct RoutingArgs {
   int n_shared;          // shared experts: groups E .. E + n_shared - 1 of T rows each
   int32_t* row_token;  // [S_max]
   float* row_gate;     // [S_max]
-  void* Xp;            // [S_max][d]
+  void* Xp;            // [S_max][d_rows]
   // outputs
   int32_t* dropped;
   float* aux;
@@ -178,6 +180,11 @@ cudaError_t launch_gemm_tc(const TcGemmPlan& plan, int num_sms, cudaStream_t s);
 bool make_map_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t rows, uint64_t cols,
                  uint32_t elem_bytes, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle);
 
+// Tensor of bytes of rank 2 or 3 (dims innermost first, strides in bytes from
+// the second dimension on) -> map with the given box and 128-byte swizzle.
+bool make_map_u8(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                 const uint32_t* box);
+
 // ---------------------------------------------------------------- 4-bit weights
 // Codes in tiles of 128 rows x 64 elements, each tile 4 KB contiguous (row r
 // of the tile at 32 r bytes): uint32 [rows / 128][K / 64][128][8]; in a word,
@@ -308,5 +315,8 @@ inline cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_
 
 // Set the calling thread's moe_last_error() message.
 void set_error_message(const char* msg);
+
+// The current device's SM count and error word.
+cudaError_t current_device_info(int* num_sms, unsigned int** err);
 
 }  // namespace moe

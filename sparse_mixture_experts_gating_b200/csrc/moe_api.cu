@@ -19,6 +19,7 @@
 #include "internal.h"
 #include "scan_dispatch.h"
 #include "backward.h"
+#include "fp8.h"
 
 struct moe_layer {
   int E, k, d, d_ff, act, gate_mode, dtype;
@@ -83,9 +84,11 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 // The second projection splits its K range for at most this many tiles.
 constexpr int kSplitMaxTiles = 4 * kSplitTargetCtas;
 
-// (4-bit weights always go through the fp32 rows and the combine.)
-bool need_yp_of(const moe_layer& L, bool w4) {
-  return w4 || !(L.dtype == MOE_BF16 && L.k == 1 && L.n_shared == 0);
+// (4-bit and 8-bit weights always go through the fp32 rows and the combine.)
+enum Weights { W_NATIVE = 0, W_INT4 = 1, W_FP8 = 2 };
+
+bool need_yp_of(const moe_layer& L, Weights kind) {
+  return kind != W_NATIVE || !(L.dtype == MOE_BF16 && L.k == 1 && L.n_shared == 0);
 }
 
 // K ranges of the 4-bit second projection: its tiles are (group, n-tile of
@@ -109,14 +112,21 @@ int w4_ksplit(int64_t s, int groups, int d, int d_ff) {
   return static_cast<int>(best);
 }
 
-int ksplit_of(const moe_layer& L, int64_t s_max, bool w4) {
-  if (w4) return w4_ksplit(s_max, L.E + L.n_shared, L.d, L.d_ff);
-  return (L.dtype == MOE_BF16 && need_yp_of(L, false)) ? gemm2_ksplit(s_max, L.E + L.n_shared, L.d, L.d_ff) : 1;
+int ksplit_of(const moe_layer& L, int64_t s_max, Weights kind) {
+  if (kind == W_INT4) return w4_ksplit(s_max, L.E + L.n_shared, L.d, L.d_ff);
+  if (kind == W_FP8) return fp8_ksplit(s_max, L.E + L.n_shared, L.d, L.d_ff);
+  return (L.dtype == MOE_BF16 && need_yp_of(L, kind)) ? gemm2_ksplit(s_max, L.E + L.n_shared, L.d, L.d_ff) : 1;
 }
 
 // Yp rows a batch of s rows needs (0: none, the bf16 rows go straight into y).
-int64_t yp_rows_of(const moe_layer& L, int64_t s, bool w4) {
-  return need_yp_of(L, w4) ? ksplit_of(L, s, w4) * s : 0;
+int64_t yp_rows_of(const moe_layer& L, int64_t s, Weights kind) {
+  return need_yp_of(L, kind) ? ksplit_of(L, s, kind) * s : 0;
+}
+
+// A row of x in the 8-bit path: its codes, then one scale for each 128 of
+// them, in one row of `x_pitch` bytes that the dispatch copies as it is.
+int64_t fp8_x_pitch(const moe_layer& L) {
+  return (L.d + static_cast<int64_t>(sizeof(float)) * ((L.d + F8_GROUP - 1) / F8_GROUP) + 15) / 16 * 16;
 }
 
 // The automatic hidden mode holds the hidden activation in fp16 when the
@@ -151,7 +161,7 @@ struct Layout {
   int ksplit;
   int ks1;     // few-row products: K ranges of the first projection
   size_t idx, gate, dest, row_token, row_gate, part_hist, part_cnt1, part_psum, part_lse2, blockoff, counts,
-      offsets, mprefix, scal, wsplit, rpart, spart, Xp, Hp, Hp_lo, Yp, W2h, P, total;
+      offsets, mprefix, scal, wsplit, rpart, spart, Xp, Hp, Hp_lo, Yp, W2h, P, Xq, Hs, total;
 };
 
 // Batches of 4-bit layers up to kW4SmallMaxT tokens take the few-row products.
@@ -179,9 +189,12 @@ SmallSplits small_splits_of(const moe_layer& L, int64_t T) {
   return r;
 }
 
-// w4: the layout of moe_forward_w4 (4-bit weights: hidden as a hi + lo pair,
-// fp32 rows for the combine, no fp16 image of W2).
-Layout make_layout(const moe_layer& L, int64_t T, bool w4 = false) {
+// kind W_INT4: the layout of moe_forward_w4 (4-bit weights: hidden as a hi + lo
+// pair, fp32 rows for the combine, no fp16 image of W2); W_FP8: that of
+// moe_forward_fp8 (x and the hidden activation as codes with scales, fp32 rows
+// for the combine).
+Layout make_layout(const moe_layer& L, int64_t T, Weights kind = W_NATIVE) {
+  const bool w4 = kind == W_INT4, fp8 = kind == W_FP8;
   Layout w;
   w.T = T;
   w.capacity = capacity_of(L, T);
@@ -191,8 +204,8 @@ Layout make_layout(const moe_layer& L, int64_t T, bool w4 = false) {
   w.s_max += static_cast<int64_t>(L.n_shared) * T;  // every token's rows of the shared experts
   w.nblk = static_cast<int>((T + kRouterTokens - 1) / kRouterTokens);
   const size_t elt = L.dtype == MOE_BF16 ? 2 : 4;
-  w.f16 = !w4 && f16_hidden_of(L, w.s_max);
-  w.split = L.dtype == MOE_BF16 &&
+  w.f16 = kind == W_NATIVE && f16_hidden_of(L, w.s_max);
+  w.split = L.dtype == MOE_BF16 && !fp8 &&
             (w4 || (!w.f16 && (L.hidden == MOE_HIDDEN_BF16X2 || L.hidden == MOE_HIDDEN_AUTO)));
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align256(o + bytes); return at; };
@@ -216,30 +229,30 @@ Layout make_layout(const moe_layer& L, int64_t T, bool w4 = false) {
   w.wsplit = take(tc_router ? 3 * sizeof(uint16_t) * router_pad_e(L.E) * static_cast<size_t>(L.d) : 0);
   w.rpart = take(tc_router ? router_partials_bytes(T, L.E, L.d) : 0);
   w.spart = take(route_small_partials_bytes(L.E));  // batches of <= 32 tokens (constant: sizes stay monotone)
-  w.Xp = take(elt * static_cast<size_t>(w.s_max) * L.d);
-  w.Hp = take(elt * static_cast<size_t>(w.s_max) * L.d_ff);
+  w.Xp = take(fp8 ? static_cast<size_t>(w.s_max) * fp8_x_pitch(L) : elt * static_cast<size_t>(w.s_max) * L.d);
+  w.Hp = take((fp8 ? 1 : elt) * static_cast<size_t>(w.s_max) * L.d_ff);
   // The automatic mode keeps the lo plane's room once it switches to fp16
   // (the largest pair any smaller batch uses), so sizes never shrink as T grows.
   int64_t lo_rows = w.split ? w.s_max : 0;
-  if (!w4 && L.dtype == MOE_BF16 && L.hidden == MOE_HIDDEN_AUTO && w.f16)
+  if (kind == W_NATIVE && L.dtype == MOE_BF16 && L.hidden == MOE_HIDDEN_AUTO && w.f16)
     lo_rows = kAutoF16RowsPerGroup * (L.E + L.n_shared) - 1;
   w.Hp_lo = take(elt * static_cast<size_t>(lo_rows) * L.d_ff);
-  w.ksplit = ksplit_of(L, w.s_max, w4);
-  w.need_yp = need_yp_of(L, w4);
+  w.ksplit = ksplit_of(L, w.s_max, kind);
+  w.need_yp = need_yp_of(L, kind);
   // Yp holds ksplit partials of s_max rows; reserve the most any smaller batch
   // needs as well, so a workspace sized for some T serves every smaller batch.
   // ksplit(s) depends on s through the m-tile bound min(G, s) + floor((s - min(G, s)) / 128)
   // (G groups), which changes at every s up to G and then every 128 rows, and
   // ksplit(s) = 1 once the bound reaches kSplitMaxTiles; the product ksplit(s) * s
   // peaks at the last s before each change.
-  int64_t yp_rows = yp_rows_of(L, w.s_max, w4);
+  int64_t yp_rows = yp_rows_of(L, w.s_max, kind);
   const int64_t groups = L.E + L.n_shared;
-  for (int64_t s = 1; s < w.s_max && s <= groups; ++s) yp_rows = std::max<int64_t>(yp_rows, yp_rows_of(L, s, w4));
+  for (int64_t s = 1; s < w.s_max && s <= groups; ++s) yp_rows = std::max<int64_t>(yp_rows, yp_rows_of(L, s, kind));
   for (int64_t s = groups + 127; s < w.s_max && s <= groups + int64_t{kSplitMaxTiles} * 128; s += 128)
-    yp_rows = std::max<int64_t>(yp_rows, yp_rows_of(L, s, w4));
+    yp_rows = std::max<int64_t>(yp_rows, yp_rows_of(L, s, kind));
   if (w4) {  // the 4-bit split also changes at every 16 / 32 / 64 rows (n-tile sizes) up to two waves of tiles
     for (int64_t s = groups + 1; s < w.s_max && s <= groups + int64_t{2 * kSplitTargetCtas} * 64; ++s)
-      yp_rows = std::max<int64_t>(yp_rows, yp_rows_of(L, s, w4));
+      yp_rows = std::max<int64_t>(yp_rows, yp_rows_of(L, s, kind));
   }
   // fp16 image of W2 (every expert, shared ones included) for the fp16 mode
   w.W2h = take(w.f16 ? sizeof(uint16_t) * static_cast<size_t>(L.E + L.n_shared) * L.d * L.d_ff : 0);
@@ -265,6 +278,8 @@ Layout make_layout(const moe_layer& L, int64_t T, bool w4 = false) {
   }
   w.Yp = take(yp_rows > 0 ? sizeof(float) * static_cast<size_t>(yp_rows) * L.d : 0);
   w.P = take(p_bytes);
+  w.Xq = take(fp8 ? static_cast<size_t>(T) * fp8_x_pitch(L) : 0);
+  w.Hs = take(fp8 ? sizeof(float) * static_cast<size_t>(w.s_max) * ((L.d_ff + F8_GROUP - 1) / F8_GROUP) : 0);
   w.total = o;
   return w;
 }
@@ -356,6 +371,15 @@ void record(const moe_debug* dbg, int stage, int which, cudaStream_t s) {
 }  // namespace
 
 void set_error_message(const char* msg) { t_err = msg; }
+
+cudaError_t current_device_info(int* num_sms, unsigned int** err) {
+  DeviceInfo* di = nullptr;
+  const cudaError_t e = device_info(&di);
+  if (e != cudaSuccess) return e;
+  *num_sms = di->num_sms;
+  *err = di->err;
+  return cudaSuccess;
+}
 
 int gemm2_ksplit(int64_t s_max, int E, int d, int d_ff) {
   // Most m-tiles the second projection can have: a group of c rows takes
@@ -475,12 +499,12 @@ size_t moe_workspace_bytes(moe_handle h, int64_t T) {
 
 namespace {
 
-// The expert weights of one forward call: bf16 / fp32 tensors, or 4-bit codes
-// with their scales (moe_forward_w4).
+// The expert weights of one forward call: bf16 / fp32 tensors, or 4-bit or
+// 8-bit codes with their scales (moe_forward_w4, moe_forward_fp8).
 struct ExpertWeights {
-  bool w4;
+  Weights kind;
   const void *W1, *W3, *W2;   // bf16 / fp32
-  const void *Q1, *Q3, *Q2;   // 4-bit codes
+  const void *Q1, *Q3, *Q2;   // codes
   const void *S1, *S3, *S2;   // their scales
 };
 
@@ -505,14 +529,25 @@ int forward_impl(moe_handle h, int64_t T, const void* x, const float* W_r, const
     t_err.clear();
     return MOE_OK;
   }
-  const void* W1 = ew.w4 ? ew.Q1 : ew.W1;
-  const void* W3 = ew.w4 ? ew.Q3 : ew.W3;
-  const void* W2 = ew.w4 ? ew.Q2 : ew.W2;
+  const bool w4 = ew.kind == W_INT4, fp8 = ew.kind == W_FP8;
+  const void* W1 = ew.kind != W_NATIVE ? ew.Q1 : ew.W1;
+  const void* W3 = ew.kind != W_NATIVE ? ew.Q3 : ew.W3;
+  const void* W2 = ew.kind != W_NATIVE ? ew.Q2 : ew.W2;
   if (x == nullptr || W_r == nullptr || W1 == nullptr || W2 == nullptr || y == nullptr)
     return fail(MOE_ERR_INVALID_ARG, F + "x, W_r, W1, W2 and y must be non-NULL");
   if ((L.act == MOE_ACT_SWIGLU) != (W3 != nullptr))
     return fail(MOE_ERR_INVALID_ARG, F + "W3 must be given for SwiGLU and NULL for ReLU");
-  if (ew.w4) {
+  if (fp8) {
+    if (ew.S1 == nullptr || ew.S2 == nullptr || (W3 != nullptr && ew.S3 == nullptr))
+      return fail(MOE_ERR_INVALID_ARG, F + "every 8-bit weight needs its scales");
+    if (L.dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, F + "8-bit weights serve bf16 layers only");
+    if (L.d % 16 != 0 || L.d_ff % 16 != 0)
+      return fail(MOE_ERR_UNSUPPORTED, F + "8-bit weights need d and d_ff to be multiples of 16");
+    const uintptr_t sal = reinterpret_cast<uintptr_t>(ew.S1) | reinterpret_cast<uintptr_t>(ew.S2) |
+                          reinterpret_cast<uintptr_t>(ew.S3);
+    if ((sal & 3) != 0) return fail(MOE_ERR_INVALID_ARG, F + "scales must be 4-byte aligned");
+  }
+  if (w4) {
     if (ew.S1 == nullptr || ew.S2 == nullptr || (W3 != nullptr && ew.S3 == nullptr))
       return fail(MOE_ERR_INVALID_ARG, F + "every 4-bit weight needs its scales");
     if (L.dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, F + "4-bit weights serve bf16 layers only");
@@ -522,7 +557,7 @@ int forward_impl(moe_handle h, int64_t T, const void* x, const float* W_r, const
                           reinterpret_cast<uintptr_t>(ew.S3);
     if ((sal & 15) != 0) return fail(MOE_ERR_INVALID_ARG, F + "scales must be 16-byte aligned");
   }
-  const Layout w = make_layout(L, T, ew.w4);
+  const Layout w = make_layout(L, T, ew.kind);
   if (workspace == nullptr || workspace_bytes < w.total)
     return fail(MOE_ERR_INVALID_ARG, F + "workspace missing or smaller than moe_workspace_bytes()");
   if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
@@ -550,6 +585,8 @@ int forward_impl(moe_handle h, int64_t T, const void* x, const float* W_r, const
   r.nblk = w.nblk;
   r.x_is_bf16 = L.dtype == MOE_BF16;
   r.x = x;
+  r.x_rows = fp8 ? static_cast<const void*>(ws + w.Xq) : x;
+  r.d_rows = fp8 ? static_cast<int>(fp8_x_pitch(L) / 2) : L.d;
   r.W_r = W_r;
   r.b_r = b_r;
   r.logits_in = dbg ? dbg->logits_in : nullptr;
@@ -621,7 +658,57 @@ int forward_impl(moe_handle h, int64_t T, const void* x, const float* W_r, const
   TcGemmPlan plan1, plan2;
   W4Plan wplan1, wplan2;
   W4SmallPlan splan1, splan2;
-  if (ew.w4) {
+  Fp8Plan fplan1, fplan2;
+  if (fp8) {
+    const char* why = nullptr;
+    const int64_t pitch = fp8_x_pitch(L), hb = (L.d_ff + F8_GROUP - 1) / F8_GROUP;
+    Fp8Args a1;
+    memset(&a1, 0, sizeof(a1));
+    a1.epi = L.act == MOE_ACT_SWIGLU ? FP8_SWIGLU : FP8_RELU;
+    a1.G = L.E + L.n_shared;
+    a1.N = L.d_ff;
+    a1.K = L.d;
+    a1.a_rows = w.s_max;
+    a1.max_group_rows = T;
+    a1.A = ws + w.Xp;
+    a1.lda = pitch;
+    a1.sa = reinterpret_cast<const float*>(ws + w.Xp + L.d);  // behind the codes of each row
+    a1.sa_ld = pitch / static_cast<int64_t>(sizeof(float));
+    a1.B0 = static_cast<const uint8_t*>(ew.Q1);
+    a1.B1 = static_cast<const uint8_t*>(ew.Q3);
+    a1.ldb = L.d;
+    a1.gsb = static_cast<int64_t>(L.d) * L.d_ff;
+    a1.sb0 = static_cast<const float*>(ew.S1);
+    a1.sb1 = static_cast<const float*>(ew.S3);
+    a1.b_rows = F8_GROUP;
+    a1.out = ws + w.Hp;
+    a1.ld_out = L.d_ff;
+    a1.out_scales = reinterpret_cast<float*>(ws + w.Hs);
+    a1.ksplit = 1;
+    a1.offsets = r.offsets;
+    a1.err = di->err;
+    Fp8Args a2 = a1;
+    a2.epi = FP8_F32;
+    a2.N = L.d;
+    a2.K = L.d_ff;
+    a2.A = ws + w.Hp;
+    a2.lda = L.d_ff;
+    a2.sa = reinterpret_cast<const float*>(ws + w.Hs);
+    a2.sa_ld = hb;
+    a2.B0 = static_cast<const uint8_t*>(ew.Q2);
+    a2.B1 = nullptr;
+    a2.ldb = L.d_ff;
+    a2.sb0 = static_cast<const float*>(ew.S2);
+    a2.sb1 = nullptr;
+    a2.out = ws + w.Yp;
+    a2.ld_out = L.d;
+    a2.out_scales = nullptr;
+    a2.ksplit = w.ksplit;
+    a2.split_stride = static_cast<int64_t>(w.s_max) * L.d;
+    a2.row_gate = r.row_gate;
+    if (plan_fp8(a1, &fplan1, &why) != cudaSuccess || plan_fp8(a2, &fplan2, &why) != cudaSuccess)
+      return fail(MOE_ERR_UNSUPPORTED, F + (why ? why : "8-bit product plan failed"));
+  } else if (w4) {
     W4Args a1;
     memset(&a1, 0, sizeof(a1));
     a1.mode = L.act == MOE_ACT_SWIGLU ? W4_SWIGLU : W4_RELU;
@@ -676,7 +763,7 @@ int forward_impl(moe_handle h, int64_t T, const void* x, const float* W_r, const
       return fail(MOE_ERR_UNSUPPORTED, std::string(F + "") + (why ? why : "GEMM plan failed"));
   }
 
-  const bool tc = L.dtype == MOE_BF16 && !ew.w4;  // bf16 expert products on the tensor-core grouped GEMM
+  const bool tc = L.dtype == MOE_BF16 && ew.kind == W_NATIVE;  // bf16 expert products on the tensor-core grouped GEMM
   const bool tc_router = L.dtype == MOE_BF16;     // every bf16 layer routes on the tensor cores (E <= 128)
   auto check = [&](cudaError_t e, const char* what) -> int {
     if (e == cudaSuccess) return MOE_OK;
@@ -684,6 +771,22 @@ int forward_impl(moe_handle h, int64_t T, const void* x, const float* W_r, const
   };
   int rc;
   record(dbg, MOE_STAGE_ROUTER, 0, s);
+  if (fp8) {  // codes and scales of x, in the packed rows that the dispatch copies
+    QuantFp8Args qa;
+    memset(&qa, 0, sizeof(qa));
+    qa.x = x;
+    qa.x_is_bf16 = 1;
+    qa.G = 1;
+    qa.R = static_cast<int>(T);
+    qa.K = L.d;
+    qa.ldx = L.d;
+    qa.block_rows = 1;
+    qa.codes = ws + w.Xq;
+    qa.ldc = fp8_x_pitch(L);
+    qa.scales = reinterpret_cast<float*>(ws + w.Xq + L.d);
+    qa.lds = qa.ldc / static_cast<int64_t>(sizeof(float));
+    if ((rc = check(launch_quantize_fp8(qa, s), "quantisation of x")) != MOE_OK) return rc;
+  }
   if (T <= kRouteSmallMaxT) {
     // one router block: router, scan and dispatch in two launches (the scan
     // and dispatch stages of the debug events stay empty)
@@ -728,7 +831,8 @@ int forward_impl(moe_handle h, int64_t T, const void* x, const float* W_r, const
                           static_cast<int64_t>(w.s_max) * L.d_ff, r.offsets + (L.E + L.n_shared), w.s_max, L.d_ff,
                           ws + w.Hp, ws + w.Hp_lo, di->num_sms, s);
   } else {
-    ce = ew.w4 ? launch_w4_gemm(wplan1, di->num_sms, s)
+    ce = fp8  ? launch_fp8(fplan1, di->num_sms, s)
+         : w4 ? launch_w4_gemm(wplan1, di->num_sms, s)
                : tc ? launch_gemm_tc(plan1, di->num_sms, s) : launch_gemm_simt(g1, w.s_max, s);
   }
   if ((rc = check(ce, "gemm1")) != MOE_OK) return rc;
@@ -740,7 +844,8 @@ int forward_impl(moe_handle h, int64_t T, const void* x, const float* W_r, const
   record(dbg, MOE_STAGE_GEMM1, 1, s);
   record(dbg, MOE_STAGE_GEMM2, 0, s);
   ce = w.small ? launch_w4_small(splan2, di->num_sms, s)
-       : ew.w4  ? launch_w4_gemm(wplan2, di->num_sms, s)
+       : fp8    ? launch_fp8(fplan2, di->num_sms, s)
+       : w4     ? launch_w4_gemm(wplan2, di->num_sms, s)
        : tc     ? launch_gemm_tc(plan2, di->num_sms, s)
                 : launch_gemm_simt(g2, w.s_max, s);
   if ((rc = check(ce, "gemm2")) != MOE_OK) return rc;
@@ -785,7 +890,7 @@ int moe_forward(moe_handle h, int64_t T, const void* x, const float* W_r, const 
 
 size_t moe_workspace_bytes_w4(moe_handle h, int64_t T) {
   if (h == nullptr || T < 0) return 0;
-  return make_layout(*h, T, true).total;
+  return make_layout(*h, T, W_INT4).total;
 }
 
 int moe_forward_w4(moe_handle h, int64_t T, const void* x, const float* W_r, const float* b_r,
@@ -795,7 +900,7 @@ int moe_forward_w4(moe_handle h, int64_t T, const void* x, const float* W_r, con
                    const moe_debug* dbg, void* stream) {
   ExpertWeights ew;
   memset(&ew, 0, sizeof(ew));
-  ew.w4 = true;
+  ew.kind = W_INT4;
   ew.Q1 = W1_codes;
   ew.Q3 = W3_codes;
   ew.Q2 = W2_codes;
@@ -804,6 +909,28 @@ int moe_forward_w4(moe_handle h, int64_t T, const void* x, const float* W_r, con
   ew.S2 = W2_scales;
   return forward_impl(h, T, x, W_r, b_r, ew, y, expert_counts, dropped, aux_loss, z_loss, workspace,
                       workspace_bytes, dbg, stream, "moe_forward_w4");
+}
+
+size_t moe_workspace_bytes_fp8(moe_handle h, int64_t T) {
+  if (h == nullptr || T < 0) return 0;
+  return make_layout(*h, T, W_FP8).total;
+}
+
+int moe_forward_fp8(moe_handle h, int64_t T, const void* x, const float* W_r, const float* b_r, const void* W1_codes,
+                    const float* W1_scales, const void* W3_codes, const float* W3_scales, const void* W2_codes,
+                    const float* W2_scales, void* y, int32_t* expert_counts, int32_t* dropped, float* aux_loss,
+                    float* z_loss, void* workspace, size_t workspace_bytes, const moe_debug* dbg, void* stream) {
+  ExpertWeights ew;
+  memset(&ew, 0, sizeof(ew));
+  ew.kind = W_FP8;
+  ew.Q1 = W1_codes;
+  ew.Q3 = W3_codes;
+  ew.Q2 = W2_codes;
+  ew.S1 = W1_scales;
+  ew.S3 = W3_scales;
+  ew.S2 = W2_scales;
+  return forward_impl(h, T, x, W_r, b_r, ew, y, expert_counts, dropped, aux_loss, z_loss, workspace,
+                      workspace_bytes, dbg, stream, "moe_forward_fp8");
 }
 
 int moe_quantize_int4(const void* W, int64_t rows, int64_t K, uint32_t* codes, void* scales, void* stream) {

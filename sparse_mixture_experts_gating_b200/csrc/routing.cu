@@ -464,7 +464,7 @@ __device__ __forceinline__ void zero_row(XT* __restrict__ y, int d, int64_t tok,
 }
 
 // ---------------------------------------------------------------------------
-// One warp copies row `tok` of x to row `dest` of the expert-sorted buffer
+// One warp copies row `tok` of x_rows (x itself, or its 8-bit image) to row `dest` of the expert-sorted buffer
 // (rows of 16-byte multiples: up to eight 16-byte loads in flight per lane).
 template <typename XT>
 __device__ __forceinline__ void copy_x_row(const XT* __restrict__ x, XT* __restrict__ Xp, int d, int64_t tok,
@@ -569,10 +569,10 @@ __global__ void __launch_bounds__(256) dispatch_kernel(RoutingArgs a) {
     }
   }
   __syncthreads();
-  const XT* x = static_cast<const XT*>(a.x);
+  const XT* x = static_cast<const XT*>(a.x_rows);
   XT* Xp = static_cast<XT*>(a.Xp);
   XT* yz = static_cast<XT*>(a.y_zero_dropped);
-  auto copy_row = [&](int64_t tok, int64_t dest) { copy_x_row(x, Xp, d, tok, dest, lane); };
+  auto copy_row = [&](int64_t tok, int64_t dest) { copy_x_row(x, Xp, a.d_rows, tok, dest, lane); };
   for (int ai = warp; ai < nA; ai += 8) {
     const int dest = dest_s[ai];
     const int64_t tok = t0 + ai / k;
@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(SCAN_T) scan_dispatch_kernel(RoutingArgs a) {
     }
   }
   __syncthreads();
-  const XT* x = static_cast<const XT*>(a.x);
+  const XT* x = static_cast<const XT*>(a.x_rows);
   XT* Xp = static_cast<XT*>(a.Xp);
   XT* yz = static_cast<XT*>(a.y_zero_dropped);
   const int gw = static_cast<int>(blockIdx.y) * (SCAN_T / 32) + warp, nw = static_cast<int>(gridDim.y) * (SCAN_T / 32);
@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(SCAN_T) scan_dispatch_kernel(RoutingArgs a) {
     const int dest = s_dest[ai];
     const int64_t tok = t0 + ai / k;
     if (dest >= 0) {
-      copy_x_row(x, Xp, d, tok, dest, lane);
+      copy_x_row(x, Xp, a.d_rows, tok, dest, lane);
     } else if (yz != nullptr) {  // k == 1: a dropped token's output row is zero
       zero_row(yz, d, tok, lane);
       if (a.yf_zero_dropped != nullptr)
@@ -770,7 +770,7 @@ __global__ void __launch_bounds__(SCAN_T) scan_dispatch_kernel(RoutingArgs a) {
         a.row_token[row] = static_cast<int32_t>(tok);
         a.row_gate[row] = 1.f;
       }
-      copy_x_row(x, Xp, d, tok, row, lane);
+      copy_x_row(x, Xp, a.d_rows, tok, row, lane);
     }
   }
 }
@@ -946,10 +946,10 @@ __global__ void __launch_bounds__(SCAN_T) route_small_kernel(RoutingArgs a, int 
   }
   __syncthreads();
   // row copies (a warp per row): kept assignments, then the shared experts' rows
-  const XT* x = static_cast<const XT*>(a.x);
+  const XT* x = static_cast<const XT*>(a.x_rows);
   XT* Xp = static_cast<XT*>(a.Xp);
   XT* yz = static_cast<XT*>(a.y_zero_dropped);
-  auto copy_row = [&](int64_t tok, int64_t dest) { copy_x_row(x, Xp, d, tok, dest, lane); };
+  auto copy_row = [&](int64_t tok, int64_t dest) { copy_x_row(x, Xp, a.d_rows, tok, dest, lane); };
   for (int i = warp; i < nA; i += SCAN_T / 32) {
     const int64_t tok = i / k;
     if (s_dest[i] >= 0) {

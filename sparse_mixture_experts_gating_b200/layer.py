@@ -5,6 +5,7 @@ provides device memory and the current stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional
 
@@ -17,6 +18,7 @@ ACT = {"relu": 0, "swiglu": 1}
 GATE = {"switch": 0, "renorm": 1}
 DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 HIDDEN = {"bf16x2": 0, "bf16": 1, "f16": 2, "auto": 3}
+FP8 = torch.float8_e4m3fn
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -26,6 +28,36 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 def _stream_handle(stream) -> int:
     s = torch.cuda.current_stream() if stream is None else stream
     return s.cuda_stream
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """Run on ``device`` and on ``stream`` (None: that device's current stream),
+    with torch's allocations on the same stream; yields the stream's handle."""
+    with contextlib.ExitStack() as stack:
+        if device.index is not None and device.index != torch.cuda.current_device():
+            stack.enter_context(torch.cuda.device(device))
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+            stack.enter_context(torch.cuda.stream(stream))
+        yield torch.cuda.current_stream(device).cuda_stream
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _check_tensor(name, t, device, dtypes, shape=None, contiguous=True):
+    """A device tensor of one of the dtypes, the shape and (by default) contiguous."""
+    if not isinstance(t, torch.Tensor) or t.device != device or device.type != "cuda":
+        raise ValueError(f"{name}: want a tensor on {device if device.type == 'cuda' else 'a CUDA device'}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: want {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: want shape {tuple(shape)}, got {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name}: want a contiguous tensor")
 
 
 def _debug_struct(debug: Optional[dict], events, stream) -> Optional[MoEDebug]:
@@ -70,6 +102,7 @@ class MoELayer:
         self._h = h
         self._ws = None
         self._bw = None  # backward scratch
+        self._last = None  # the workspace of forward_fp8's last call without one of the caller's
         self.hidden = hidden
         check(lib().moe_set_hidden_precision(h, HIDDEN[hidden]))
         self.n_shared = int(n_shared)
@@ -113,6 +146,8 @@ class MoELayer:
                      torch.empty(1, dtype=torch.float32, device=dev))
         counts, dropped, aux, z = stats
         ws = workspace if workspace is not None else self.workspace(T, dev)
+        if workspace is None:
+            self._last = None  # (balance_losses reads self._ws)
         dbg = _debug_struct(debug, events, stream)
         check(lib().moe_forward(
             self._h, T, _ptr(x), _ptr(W_r), _ptr(b_r), _ptr(W1), _ptr(W3), _ptr(W2), _ptr(y),
@@ -143,12 +178,57 @@ class MoELayer:
             if self._ws is None or self._ws.numel() < n or self._ws.device != dev:
                 self._ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
             workspace = self._ws
+            self._last = None
         dbg = _debug_struct(debug, events, stream)
         q3, s3 = (None, None) if W3q is None else W3q
         check(lib().moe_forward_w4(
             self._h, T, _ptr(x), _ptr(W_r), _ptr(b_r), _ptr(W1q[0]), _ptr(W1q[1]), _ptr(q3), _ptr(s3),
             _ptr(W2q[0]), _ptr(W2q[1]), _ptr(y), _ptr(counts), _ptr(dropped), _ptr(aux), _ptr(z),
             _ptr(workspace), workspace.numel(), None if dbg is None else ctypes.byref(dbg), _stream_handle(stream)))
+        return y, counts, dropped, aux, z
+
+    def workspace_bytes_fp8(self, T: int) -> int:
+        return int(lib().moe_workspace_bytes_fp8(self._h, T))
+
+    def forward_fp8(self, x, W_r, b_r, W1q, W3q, W2q, *, out=None, stats=None, workspace=None,
+                    debug: Optional[dict] = None, events=None, stream=None):
+        """The layer with 8-bit expert weights: W1q, W3q (None for ReLU), W2q are
+        (codes, scales) pairs from quantize_fp8(W, block_rows=128); x and the
+        hidden activation are quantised on the way.  Returns like forward().
+        Without ``workspace`` every call takes its own from torch's allocator,
+        so calls on several streams or in several captured graphs share none."""
+        T, dev = x.shape[0], x.device
+        G = self.E + self.n_shared
+        _check_tensor("x", x, dev, (torch.bfloat16,), (T, self.d))
+        _check_tensor("W_r", W_r, dev, (torch.float32,), (self.E, self.d))
+        if b_r is not None:
+            _check_tensor("b_r", b_r, dev, (torch.float32,), (self.E,))
+        for name, q, rows, cols in (("W1q", W1q, self.d_ff, self.d), ("W3q", W3q, self.d_ff, self.d),
+                                    ("W2q", W2q, self.d, self.d_ff)):
+            if q is not None:
+                _check_tensor(name + " codes", q[0], dev, (FP8,), (G, rows, cols))
+                _check_tensor(name + " scales", q[1], dev, (torch.float32,), (G, _blocks(rows), _blocks(cols)))
+        if W1q is None or W2q is None:
+            raise ValueError("forward_fp8: W1q and W2q are (codes, scales) pairs")
+        if out is not None:
+            _check_tensor("out", out, dev, (torch.bfloat16,), (T, self.d))
+        with _on(dev, stream) as handle:
+            y = out if out is not None else torch.empty((T, self.d), dtype=x.dtype, device=dev)
+            if stats is None:
+                stats = (torch.empty(self.E, dtype=torch.int32, device=dev),
+                         torch.empty(1, dtype=torch.int32, device=dev),
+                         torch.empty(1, dtype=torch.float32, device=dev),
+                         torch.empty(1, dtype=torch.float32, device=dev))
+            counts, dropped, aux, z = stats
+            if workspace is None:
+                workspace = torch.empty(max(self.workspace_bytes_fp8(T), 256), dtype=torch.uint8, device=dev)
+                self._last = workspace
+            dbg = _debug_struct(debug, events, stream)
+            q3, s3 = (None, None) if W3q is None else W3q
+            check(lib().moe_forward_fp8(
+                self._h, T, _ptr(x), _ptr(W_r), _ptr(b_r), _ptr(W1q[0]), _ptr(W1q[1]), _ptr(q3), _ptr(s3),
+                _ptr(W2q[0]), _ptr(W2q[1]), _ptr(y), _ptr(counts), _ptr(dropped), _ptr(aux), _ptr(z),
+                _ptr(workspace), workspace.numel(), None if dbg is None else ctypes.byref(dbg), handle))
         return y, counts, dropped, aux, z
 
     def backward_workspace_bytes(self, T: int) -> int:
@@ -186,7 +266,7 @@ class MoELayer:
         """The alternative balance statistics of the last forward on ``workspace``
         (default: this layer's own): a device tensor [aux over all k choices,
         CV of the assignment counts, cv^2 of the mean router probabilities]."""
-        ws = workspace if workspace is not None else self._ws
+        ws = workspace if workspace is not None else self._last if self._last is not None else self._ws
         dev = ws.device if ws is not None else torch.device("cuda")
         out = out if out is not None else torch.empty(3, dtype=torch.float32, device=dev)
         check(lib().moe_balance_losses(self._h, T, _ptr(ws), _ptr(out), _stream_handle(stream)))
@@ -218,6 +298,97 @@ def quantize_int4(W: torch.Tensor, stream=None):
     scales = torch.empty(lead + (K // 128,), dtype=torch.bfloat16, device=W.device)
     check(lib().moe_quantize_int4(_ptr(W.contiguous()), rows, K, _ptr(codes), _ptr(scales), _stream_handle(stream)))
     return codes, scales
+
+
+def _rows_of(t: torch.Tensor):
+    """(matrices, rows, columns, row stride) of a tensor read as matrices
+    [rows][columns] laid out one after another, or None if it is not."""
+    if t.dim() < 2 or t.stride(-1) != 1 and t.shape[-1] > 1:
+        return None
+    rows, cols = t.shape[-2:]
+    ld = t.stride(-2) if rows > 1 else max(t.stride(-2), cols)
+    if ld < cols:
+        return None
+    if t.numel() == cols:  # one row: its stride says nothing
+        ld = (cols + 15) // 16 * 16
+    mats, step = 1, rows * ld
+    for n, s in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        if n != 1 and s != step:
+            return None
+        mats, step = mats * n, step * n
+    return mats, rows, cols, ld
+
+
+def quantize_fp8(x: torch.Tensor, *, block_rows: int = 1, transpose: bool = False, stream=None):
+    """e4m3 codes and fp32 scales of x [..., R, K] (bf16 or fp32): one scale for
+    each 128 elements of a row (block_rows 1, activations and gradients) or for
+    each 128 x 128 block (block_rows 128, weights).  transpose: of x's
+    transposed matrices [..., K, R].  The codes' rows start on 16-byte
+    boundaries (a view of a wider tensor where the row length is no multiple
+    of 16); scales are [..., ceil(rows / block_rows), ceil(columns / 128)]."""
+    dev = x.device
+    _check_tensor("x", x, dev, (torch.bfloat16, torch.float32), contiguous=False)
+    if x.dim() < 2:
+        raise ValueError("quantize_fp8: x needs at least two dimensions")
+    if block_rows not in (1, 128):
+        raise ValueError("quantize_fp8: block_rows must be 1 or 128")
+    with _on(dev, stream) as handle:
+        form = _rows_of(x)
+        if form is None:
+            x = x.contiguous()
+            form = _rows_of(x)
+        mats, R, K, ld = form
+        rows, cols = (K, R) if transpose else (R, K)
+        pitch = (cols + 15) // 16 * 16
+        codes = torch.empty(x.shape[:-2] + (rows, pitch), dtype=FP8, device=dev)[..., :cols]
+        scales = torch.empty(x.shape[:-2] + ((rows + block_rows - 1) // block_rows, _blocks(cols)),
+                             dtype=torch.float32, device=dev)
+        check(lib().moe_quantize_fp8(_ptr(x), DTYPE[x.dtype], mats, R, K, ld, block_rows, int(transpose), _ptr(codes),
+                                     pitch, _ptr(scales), handle))
+    return codes, scales
+
+
+def matmul_fp8(a, b, *, offsets: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, out=None, stream=None):
+    """a [M, K] times b [N, K] transposed, both (codes, scales) pairs of
+    quantize_fp8: a with block_rows 1, b with 128 or 1.  With offsets (int32
+    [G + 1] on the device, ascending) b is [G, N, K] and rows offsets[g] ..
+    offsets[g + 1] - 1 of a are multiplied by b[g]; rows of no group are left as
+    they were in ``out``.  Returns [M, N] in out_dtype (bf16 or fp32)."""
+    (ac, sa), (bc, sb) = a, b
+    dev = ac.device
+    _check_tensor("a codes", ac, dev, (FP8,), contiguous=False)
+    _check_tensor("b codes", bc, dev, (FP8,), contiguous=False)
+    if ac.dim() != 2 or bc.dim() != (2 if offsets is None else 3) or ac.shape[1] != bc.shape[-1]:
+        raise ValueError(f"matmul_fp8: a [M, K] and b {'[N, K]' if offsets is None else '[G, N, K]'}, got "
+                         f"{tuple(ac.shape)} and {tuple(bc.shape)}")
+    M, K = ac.shape
+    N = bc.shape[-2]
+    G = 1 if offsets is None else bc.shape[0]
+    _check_tensor("a scales", sa, dev, (torch.float32,), (M, _blocks(K)))
+    lead = tuple(bc.shape[:-2])
+    if sb.dim() != bc.dim() or sb.shape[-2] not in (N, _blocks(N)):
+        raise ValueError(f"matmul_fp8: b scales have {N} or {_blocks(N)} rows, got {tuple(sb.shape)}")
+    b_rows = 128 if sb.shape[-2] == _blocks(N) else 1
+    _check_tensor("b scales", sb, dev, (torch.float32,), lead + (sb.shape[-2], _blocks(K)))
+    if offsets is not None:
+        _check_tensor("offsets", offsets, dev, (torch.int32,), (G + 1,))
+    if out_dtype not in DTYPE:
+        raise ValueError(f"matmul_fp8: out_dtype is bf16 or fp32, got {out_dtype}")
+    fa, fb = _rows_of(ac), _rows_of(bc)
+    if fa is None or fb is None:
+        raise ValueError("matmul_fp8: the codes' rows must be contiguous, their matrices one after another")
+    if out is not None:
+        _check_tensor("out", out, dev, (out_dtype,), (M, N), contiguous=False)
+        if _rows_of(out) is None:
+            raise ValueError("matmul_fp8: out's rows must be contiguous")
+    with _on(dev, stream) as handle:
+        if out is None:
+            out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        n = int(lib().moe_matmul_fp8_workspace_bytes(M, N, K, G))
+        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        check(lib().moe_matmul_fp8(M, N, K, G, _ptr(ac), fa[3], _ptr(sa), _ptr(bc), fb[3], _ptr(sb), b_rows,
+                                   _ptr(offsets), _ptr(out), DTYPE[out_dtype], _rows_of(out)[3], _ptr(ws), n, handle))
+    return out
 
 
 def status(stream=None) -> None:
