@@ -1,0 +1,126 @@
+"""The layer's forward with 8-bit expert weights against its definition.
+
+Routing is the oracle's (bit for bit on dyadic router inputs).  The experts
+read x quantised, and quantise the hidden activation: a hidden value that lies
+within the fp32 error of a border between two codes may take either, so each
+output is allowed what those elements can move it by, and nothing more.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from sparse_mixture_experts_gating_b200 import MoEError, MoELayer, matmul_fp8, quantize_fp8, status
+from sparse_mixture_experts_gating_b200.workloads import (ACT_RELU, ACT_SWIGLU, DTYPE_BF16, GATE_RENORM, GATE_SWITCH,
+                                                          Workload, make_inputs)
+from tests import _fp8 as F
+from tests._parity import assert_gates_and_losses, assert_routing_equal, layer_for, np32
+
+pytestmark = pytest.mark.gpu
+
+R, S, SW, RN = ACT_RELU, ACT_SWIGLU, GATE_SWITCH, GATE_RENORM
+ULP = 2.0 ** -23
+
+
+def quantized(inp):
+    return {k: None if inp[k] is None else quantize_fp8(inp[k], block_rows=128) for k in ("W1", "W3", "W2")}
+
+
+def run(w, inp, q, layer=None, **kw):
+    layer = layer or layer_for(w)
+    dbg = layer.debug_buffers(w.T, inp["x"].device)
+    y, counts, dropped, aux, z = layer.forward_fp8(inp["x"], inp["W_r"], inp["b_r"], q["W1"], q["W3"], q["W2"],
+                                                   debug=dbg, **kw)
+    status()
+    g = {"y_dev": y, "counts": counts.cpu().numpy(), "dropped": int(dropped.item()), "aux": float(aux.item()),
+         "z": float(z.item())}
+    g.update({k: t.cpu().numpy() for k, t in dbg.items()})
+    bl = layer.balance_losses(w.T).cpu().numpy()
+    g.update(aux_all_choices=float(bl[0]), cv_counts=float(bl[1]), cv2_probs=float(bl[2]))
+    return g
+
+
+def host_weight(pair, e):
+    return F.values(F.decode(pair[0][e].view(torch.uint8).cpu().numpy()), pair[1][e].cpu().numpy(), 128)
+
+
+def reference(w, inp, q):
+    """(the oracle's routing, y, how far a computed y may be off) in 64 bits."""
+    x = np32(inp["x"])
+    zero = np.zeros((w.E, w.d_ff, w.d), np.float32)
+    o = O.moe_forward(x, np32(inp["W_r"]), np32(inp["b_r"]), zero, zero if w.act == S else None,
+                      np.zeros((w.E, w.d, w.d_ff), np.float32), k=w.k, gate_mode=w.gate, act=w.act,
+                      capacity_factor=w.capacity_factor)
+    xv = F.values(*F.quantize(x), 1)
+    y, tol = np.zeros((w.T, w.d)), np.zeros((w.T, w.d))
+    for e in range(w.E + w.n_shared):
+        if e < w.E:
+            rows, slot = np.nonzero((o["idx"] == e) & o["kept"])
+            gate = o["gate"][rows, slot][:, None]
+        else:
+            rows, gate = np.arange(w.T), 1.0
+        if rows.size == 0:
+            continue
+        W1, W2 = host_weight(q["W1"], e), host_weight(q["W2"], e)
+        a1, e1 = xv[rows] @ W1.T, F.product_bound(xv[rows], W1)
+        if w.act == R:
+            h, eh = np.maximum(a1, 0), e1
+        else:
+            W3 = host_weight(q["W3"], e)
+            a3, e3 = xv[rows] @ W3.T, F.product_bound(xv[rows], W3)
+            s = a1 / (1 + np.exp(-a1))
+            h = s * a3
+            # |silu'| < 1.1; the fast exponential and divide are off by a few units and one per unit of |a1|
+            eh = 1.1 * np.abs(a3) * e1 + (np.abs(s) + 1.1 * e1) * e3 + np.abs(h) * (8 + 1.2 * np.abs(a1)) * ULP
+        codes, scales = F.quantize(h)
+        sc = F.spread(scales.astype(np.float64), 1, *h.shape)
+        top = F.spread(np.stack([np.abs(h[:, c:c + 128]).max(1) for c in range(0, w.d_ff, 128)], 1), 1, *h.shape)
+        etop = F.spread(np.stack([eh[:, c:c + 128].max(1) for c in range(0, w.d_ff, 128)], 1), 1, *h.shape)
+        # the value that is rounded, h / scale, and how far a computed one may be off
+        v = np.abs(h) / sc
+        ev = (eh + np.abs(h) * etop / np.maximum(top, F.TINY)) / sc + 8 * ULP * v
+        lo, hi = F.round_e4m3(np.maximum(v - ev, 0)), F.round_e4m3(np.minimum(v + ev, 448))
+        move = np.maximum(hi - np.abs(codes), np.abs(codes) - lo) * sc
+        hv = codes * sc
+        move = move + np.abs(hv) * (etop / np.maximum(top, F.TINY) + 2 * ULP)  # the scale's own error
+        yr = hv @ W2.T
+        er = F.product_bound(hv, W2) + move @ np.abs(W2).T
+        y[rows] += gate * yr
+        tol[rows] += np.abs(gate) * er + np.abs(yr) * 2e-6 + np.abs(gate * yr) * 4 * ULP
+    return o, y, tol + np.abs(y) * 8 * ULP + 1e-30
+
+
+def check(w, inp, q, g):
+    o, y, tol = reference(w, inp, q)
+    assert_routing_equal(g, o)
+    assert_gates_and_losses(g, o)
+    err = np.abs(g["y_f32"].astype(np.float64) - y)
+    assert (err <= tol).all(), (err / tol).max()
+    # few of the elements that may move do: the layer's usual bound of the mean holds as well
+    assert err.sum() <= 2e-3 * np.abs(y).sum(), err.sum() / np.abs(y).sum()
+    assert torch.equal(torch.from_numpy(g["y_f32"]).to(torch.bfloat16), g["y_dev"].cpu())
+
+
+CASES = [
+    Workload("one_token", T=1, d=256, E=8, k=2, d_ff=512, act=S, gate=RN, capacity_factor=0.0, dtype=DTYPE_BF16,
+             dyadic=True, seed=31),
+    Workload("decode", T=20, d=384, E=4, k=2, d_ff=640, act=S, gate=RN, capacity_factor=0.0, dtype=DTYPE_BF16,
+             bias="normal", dyadic=True, seed=32),
+    Workload("ragged_blocks", T=70, d=208, E=3, k=1, d_ff=176, act=S, gate=SW, capacity_factor=0.0, dtype=DTYPE_BF16,
+             dyadic=True, seed=33),
+    Workload("relu_drops", T=300, d=128, E=8, k=2, d_ff=272, act=R, gate=SW, capacity_factor=0.75, dtype=DTYPE_BF16,
+             bias="normal", dyadic=True, seed=34),
+    Workload("large_groups", T=700, d=256, E=4, k=2, d_ff=384, act=S, gate=RN, capacity_factor=1.25,
+             dtype=DTYPE_BF16, bias="normal", dyadic=True, seed=35),
+    Workload("shared", T=150, d=144, E=5, k=3, d_ff=256, act=R, gate=RN, capacity_factor=1.0, dtype=DTYPE_BF16,
+             dyadic=True, seed=36, n_shared=2),
+    Workload("tiny_rows", T=33, d=16, E=4, k=4, d_ff=16, act=S, gate=RN, capacity_factor=0.0, dtype=DTYPE_BF16,
+             dyadic=True, seed=37),
+]
+
+
+@pytest.mark.parametrize("w", CASES, ids=lambda w: w.name)
+def test_layer_matches_its_definition(w):
+    inp = make_inputs(w, device="cuda")
+    q = quantized(inp)
+    check(w, inp, q, run(w, inp, q))
