@@ -396,6 +396,57 @@ MOE_API int moe_backward(moe_handle h, int64_t T, const void* x, const float* W_
                          size_t bw_workspace_bytes, void* stream);
 
 /*
+ * moe_backward with a further gradient of the router logits: dlogits [T][E]
+ * fp32 (NULL: none) is added to the one that the loss above gives them, before
+ * it goes on to x, W_r and b_r.  moe_router_balance_backward makes one.
+ */
+MOE_API int moe_backward_logits(moe_handle h, int64_t T, const void* x, const float* W_r, const float* b_r,
+                                const void* W1, const void* W3, const void* W2, const void* dy, float aux_coef,
+                                float z_coef, const float* dlogits, float* dx, float* dW_r, float* db_r, float* dW1,
+                                float* dW3, float* dW2, const void* workspace, size_t workspace_bytes,
+                                void* bw_workspace, size_t bw_workspace_bytes, void* stream);
+
+/*
+ * The balance loss and the z-loss of every sequence of a packed batch, from
+ * router logits [T][E] (fp32 or bf16, 1 <= E <= 256, contiguous), with the
+ * per-expert counts.  Sequence b is tokens offsets[b] .. offsets[b + 1] - 1
+ * (int32 on the device, ascending, [sequences + 1]; NULL with one sequence:
+ * every token).  mask [T] (bytes; NULL: none): 0 marks padding, whose logits
+ * are not read.  For the n_b tokens of a sequence that count:
+ *   p      softmax of the logits (MOE_SCORE_SOFTMAX), or their sigmoid divided
+ *          by its sum over the experts (MOE_SCORE_SIGMOID)
+ *   counts [sequences][E] int32: choices of each expert, by the k largest
+ *          logits (ties to the lower index)
+ *   aux    [sequences] E / (k n_b) sum_e counts_be mean_t p_te; with one
+ *          sequence, no mask and softmax this is moe_balance_losses' out[0]
+ *   z      [sequences] mean_t (log sum_e exp logit_te)^2
+ *   tokens [sequences] int32: n_b
+ * An expert whose logit is -inf is never chosen and has p = 0; a token with no
+ * expert left counts as padding.  A sequence without tokens has aux = z = 0.
+ * Other non-finite logits make the results NaN.
+ *
+ * moe_router_balance_backward: dlogits [T][E] fp32, the gradient of sum_b daux_b
+ * aux_b + dz_b z_b (daux, dz [sequences] fp32; NULL: 0), the counts held
+ * fixed, from the forward's counts and tokens; 0 for padding and for tokens of
+ * no sequence.
+ *
+ * Deterministic: every sum has a fixed order.  Offsets outside [0, T] or not
+ * ascending give wrong results, never an access outside the buffers.
+ * workspace: moe_router_balance_workspace_bytes(T, E, sequences) bytes,
+ * 16-byte aligned.  Asynchronous on `stream`.
+ */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+MOE_API size_t moe_router_balance_workspace_bytes(int64_t T, int num_experts, int64_t sequences);
+MOE_API int moe_router_balance(int64_t T, int num_experts, int k, const void* logits, int dtype, int scoring,
+                               int64_t sequences, const int32_t* offsets, const uint8_t* mask, float* aux, float* z,
+                               int32_t* counts, int32_t* tokens, void* workspace, size_t workspace_bytes,
+                               void* stream);
+MOE_API int moe_router_balance_backward(int64_t T, int num_experts, int k, const void* logits, int dtype, int scoring,
+                                        int64_t sequences, const int32_t* offsets, const uint8_t* mask,
+                                        const int32_t* counts, const int32_t* tokens, const float* daux,
+                                        const float* dz, float* dlogits, void* stream);
+
+/*
  * Synchronise `stream` and report the device error word of the current device:
  * MOE_OK, MOE_ERR_TIMEOUT (a kernel's bounded wait ran out and it returned
  * early; outputs of that call are undefined), MOE_ERR_RANGE (fp16 hidden mode:

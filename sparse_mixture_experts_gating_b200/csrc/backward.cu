@@ -363,7 +363,8 @@ __global__ void __launch_bounds__(THREADS) bw_router_kernel(BackwardArgs a) {
   const float dpp = block_sum_f(pd, s_red);
   for (int e = tid; e < E; e += THREADS) {
     const float p = expf(s_h[e] - m) / Z;
-    a.dh[t * E + e] = s_dh[e] + p * (s_dp[e] - dpp) + a.z_coef * 2.f * inv_T * lse * p;
+    const float dl = s_dh[e] + p * (s_dp[e] - dpp) + a.z_coef * 2.f * inv_T * lse * p;
+    a.dh[t * E + e] = a.dlogits != nullptr ? dl + a.dlogits[t * E + e] : dl;
   }
 }
 

@@ -23,6 +23,7 @@ struct BackwardArgs {
   const void* W2;      // [E + n_shared][d][d_ff]
   const void* dy;      // [T][d]
   float aux_coef, z_coef;
+  const float* dlogits;  // [T][E] a further gradient of the router logits, or NULL
   // forward workspace
   const int32_t* topk_idx;   // [T][k]
   const float* topk_gate;    // [T][k]

@@ -993,10 +993,11 @@ size_t moe_backward_workspace_bytes(moe_handle h, int64_t T) {
   return make_bw_layout(*h, make_layout(*h, T)).total;
 }
 
-int moe_backward(moe_handle h, int64_t T, const void* x, const float* W_r, const float* b_r, const void* W1,
-                 const void* W3, const void* W2, const void* dy, float aux_coef, float z_coef, float* dx,
-                 float* dW_r, float* db_r, float* dW1, float* dW3, float* dW2, const void* workspace,
-                 size_t workspace_bytes, void* bw_workspace, size_t bw_workspace_bytes, void* stream) {
+int moe_backward_logits(moe_handle h, int64_t T, const void* x, const float* W_r, const float* b_r, const void* W1,
+                        const void* W3, const void* W2, const void* dy, float aux_coef, float z_coef,
+                        const float* dlogits, float* dx, float* dW_r, float* db_r, float* dW1, float* dW3, float* dW2,
+                        const void* workspace, size_t workspace_bytes, void* bw_workspace, size_t bw_workspace_bytes,
+                        void* stream) {
   if (h == nullptr) return fail(MOE_ERR_INVALID_ARG, "moe_backward: handle is NULL");
   const moe_layer& L = *h;
   if (T < 0) return fail(MOE_ERR_INVALID_ARG, "moe_backward: T < 0");
@@ -1067,6 +1068,7 @@ int moe_backward(moe_handle h, int64_t T, const void* x, const float* W_r, const
   a.dy = dy;
   a.aux_coef = aux_coef;
   a.z_coef = z_coef;
+  a.dlogits = dlogits;
   a.topk_idx = reinterpret_cast<const int32_t*>(ws + w.idx);
   a.topk_gate = reinterpret_cast<const float*>(ws + w.gate);
   a.dest_row = reinterpret_cast<const int32_t*>(ws + w.dest);
@@ -1139,6 +1141,14 @@ int moe_backward(moe_handle h, int64_t T, const void* x, const float* W_r, const
   if (ce != cudaSuccess) return fail(MOE_ERR_CUDA, std::string("moe_backward: ") + cudaGetErrorString(ce));
   t_err.clear();
   return MOE_OK;
+}
+
+int moe_backward(moe_handle h, int64_t T, const void* x, const float* W_r, const float* b_r, const void* W1,
+                 const void* W3, const void* W2, const void* dy, float aux_coef, float z_coef, float* dx,
+                 float* dW_r, float* db_r, float* dW1, float* dW3, float* dW2, const void* workspace,
+                 size_t workspace_bytes, void* bw_workspace, size_t bw_workspace_bytes, void* stream) {
+  return moe_backward_logits(h, T, x, W_r, b_r, W1, W3, W2, dy, aux_coef, z_coef, nullptr, dx, dW_r, db_r, dW1, dW3,
+                             dW2, workspace, workspace_bytes, bw_workspace, bw_workspace_bytes, stream);
 }
 
 }  // extern "C"

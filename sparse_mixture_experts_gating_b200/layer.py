@@ -18,6 +18,7 @@ ACT = {"relu": 0, "swiglu": 1}
 GATE = {"switch": 0, "renorm": 1}
 DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 HIDDEN = {"bf16x2": 0, "bf16": 1, "f16": 2, "auto": 3}
+SCORING = {"softmax": 0, "sigmoid": 1}
 FP8 = torch.float8_e4m3fn
 
 
@@ -235,10 +236,11 @@ class MoELayer:
         return int(lib().moe_backward_workspace_bytes(self._h, T))
 
     def backward(self, x, W_r, b_r, W1, W3, W2, dy, *, aux_coef=0.0, z_coef=0.0, workspace=None,
-                 bw_workspace=None, grads=None, stream=None) -> dict:
+                 bw_workspace=None, grads=None, stream=None, dlogits=None) -> dict:
         """Gradients of <dy, y> + aux_coef * aux + z_coef * z for the last
         forward on ``workspace`` (default: this layer's own), routing held
-        fixed.  Returns fp32 device tensors dx, dW_r, db_r (None without a
+        fixed.  dlogits [T, E] fp32: a further gradient of the router logits
+        (router_balance_backward makes one).  Returns fp32 device tensors dx, dW_r, db_r (None without a
         bias), dW1, dW3 (None for ReLU), dW2; ``grads`` may supply them."""
         T, dev = x.shape[0], x.device
         ws = workspace if workspace is not None else self._ws
@@ -247,6 +249,8 @@ class MoELayer:
             if self._bw is None or self._bw.numel() < n or self._bw.device != dev:
                 self._bw = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
             bw_workspace = self._bw
+        if dlogits is not None:
+            _check_tensor("dlogits", dlogits, dev, (torch.float32,), (T, self.E))
         f32 = dict(dtype=torch.float32, device=dev)
         g = dict(grads or {})
         g.setdefault("dx", torch.empty((T, self.d), **f32))
@@ -255,9 +259,9 @@ class MoELayer:
         g.setdefault("dW1", torch.empty(W1.shape, **f32))
         g.setdefault("dW3", None if W3 is None else torch.empty(W3.shape, **f32))
         g.setdefault("dW2", torch.empty(W2.shape, **f32))
-        check(lib().moe_backward(
+        check(lib().moe_backward_logits(
             self._h, T, _ptr(x), _ptr(W_r), _ptr(b_r), _ptr(W1), _ptr(W3), _ptr(W2), _ptr(dy),
-            float(aux_coef), float(z_coef), _ptr(g["dx"]), _ptr(g["dW_r"]), _ptr(g["db_r"]), _ptr(g["dW1"]),
+            float(aux_coef), float(z_coef), _ptr(dlogits), _ptr(g["dx"]), _ptr(g["dW_r"]), _ptr(g["db_r"]), _ptr(g["dW1"]),
             _ptr(g["dW3"]), _ptr(g["dW2"]), _ptr(ws), 0 if ws is None else ws.numel(), _ptr(bw_workspace),
             bw_workspace.numel(), _stream_handle(stream)))
         return g
@@ -389,6 +393,67 @@ def matmul_fp8(a, b, *, offsets: Optional[torch.Tensor] = None, out_dtype=torch.
         check(lib().moe_matmul_fp8(M, N, K, G, _ptr(ac), fa[3], _ptr(sa), _ptr(bc), fb[3], _ptr(sb), b_rows,
                                    _ptr(offsets), _ptr(out), DTYPE[out_dtype], _rows_of(out)[3], _ptr(ws), n, handle))
     return out
+
+
+def _balance_args(name, logits, k, offsets, mask, scoring):
+    if logits.dim() != 2:
+        raise ValueError(f"{name}: logits are [T, E]")
+    dev = logits.device
+    _check_tensor("logits", logits, dev, (torch.float32, torch.bfloat16))
+    if scoring not in SCORING:
+        raise ValueError(f"{name}: scoring is one of {sorted(SCORING)}")
+    T, E = logits.shape
+    B = 1
+    if offsets is not None:
+        if offsets.dim() != 1 or offsets.shape[0] < 1:
+            raise ValueError(f"{name}: offsets are [sequences + 1]")
+        _check_tensor("offsets", offsets, dev, (torch.int32,))
+        B = offsets.shape[0] - 1
+    if mask is not None:
+        _check_tensor("mask", mask, dev, (torch.bool, torch.uint8), (T,))
+    return dev, T, E, B
+
+
+def router_balance(logits: torch.Tensor, k: int, *, offsets: Optional[torch.Tensor] = None,
+                   mask: Optional[torch.Tensor] = None, scoring: str = "softmax", stream=None):
+    """(aux, z, counts, tokens) of every sequence of a packed batch from its router
+    logits [T, E] (fp32 or bf16): the balance loss over all k choices, the mean
+    squared log-sum-exp, the choices of each expert [sequences, E] and the
+    tokens that count.  Sequence b is tokens offsets[b] .. offsets[b + 1] - 1
+    (int32 on the device; None: one sequence); mask [T]: False marks padding;
+    scoring: "softmax" or "sigmoid" (normalised over the experts)."""
+    dev, T, E, B = _balance_args("router_balance", logits, k, offsets, mask, scoring)
+    with _on(dev, stream) as handle:
+        aux, z = torch.empty((2, B), dtype=torch.float32, device=dev)
+        counts = torch.empty((B, E), dtype=torch.int32, device=dev)
+        tokens = torch.empty(B, dtype=torch.int32, device=dev)
+        n = int(lib().moe_router_balance_workspace_bytes(T, E, B))
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        check(lib().moe_router_balance(T, E, int(k), _ptr(logits), DTYPE[logits.dtype], SCORING[scoring], B,
+                                       _ptr(offsets), _ptr(mask), _ptr(aux), _ptr(z), _ptr(counts), _ptr(tokens),
+                                       _ptr(ws), n, handle))
+    return aux, z, counts, tokens
+
+
+def router_balance_backward(logits: torch.Tensor, counts: torch.Tensor, tokens: torch.Tensor,
+                            daux: Optional[torch.Tensor], dz: Optional[torch.Tensor], k: int, *,
+                            offsets: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                            scoring: str = "softmax", stream=None) -> torch.Tensor:
+    """The gradient [T, E] fp32 of sum_b daux_b aux_b + dz_b z_b with respect to the
+    logits, from router_balance's counts and tokens (held fixed); daux and dz
+    are [sequences] fp32 or None.  Zero for padding and tokens of no sequence."""
+    dev, T, E, B = _balance_args("router_balance_backward", logits, k, offsets, mask, scoring)
+    _check_tensor("counts", counts, dev, (torch.int32,), (B, E))
+    _check_tensor("tokens", tokens, dev, (torch.int32,), (B,))
+    for name, g in (("daux", daux), ("dz", dz)):
+        if g is not None:
+            _check_tensor(name, g, dev, (torch.float32,), (B,))
+    with _on(dev, stream) as handle:
+        dlogits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        check(lib().moe_router_balance_backward(T, E, int(k), _ptr(logits), DTYPE[logits.dtype], SCORING[scoring], B,
+                                                _ptr(offsets), _ptr(mask), _ptr(counts), _ptr(tokens), _ptr(daux),
+                                                _ptr(dz), _ptr(dlogits), handle))
+    return dlogits
 
 
 def status(stream=None) -> None:

@@ -1,0 +1,202 @@
+"""The balance loss and z-loss of each sequence and their gradient, against the
+definition in 64 bits, against differences, and with the layer they serve."""
+import numpy as np
+import pytest
+import torch
+
+from sparse_mixture_experts_gating_b200 import MoELayer, router_balance, router_balance_backward, status
+from sparse_mixture_experts_gating_b200.workloads import (ACT_RELU, DTYPE_BF16, GATE_SWITCH, Workload, make_inputs)
+from tests import _balance as D
+from tests._parity import layer_for
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def make(T, E, seed, dtype, mask, minus_inf):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    l = torch.randn((T, E), device="cuda", generator=g) * 2 + torch.randn(E, device="cuda", generator=g)
+    l = l.to(dtype)
+    if minus_inf and T > 0:
+        l[torch.rand((T, E), device="cuda", generator=g) < 0.2] = float("-inf")
+        l[T // 2] = float("-inf")                      # a token with no expert left
+    m = None
+    if mask:
+        m = torch.rand(T, device="cuda", generator=g) > 0.3
+        l[~m] = float("nan")
+        if T > 3:
+            m[1], m[3] = False, False
+            l[1], l[3] = float("inf"), torch.finfo(dtype).min
+    return l, m
+
+
+def run(l, k, offsets, m, scoring, daux, dz, **kw):
+    aux, z, counts, tokens = router_balance(l, k, offsets=offsets, mask=m, scoring=scoring, **kw)
+    d = router_balance_backward(l, counts, tokens, daux, dz, k, offsets=offsets, mask=m, scoring=scoring, **kw)
+    return aux, z, counts, tokens, d
+
+
+def check(l, k, cuts, m, scoring, seed=0):
+    B = len(cuts) - 1
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    daux, dz = (torch.randn(B, device="cuda", generator=g) for _ in range(2))
+    offsets = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+    aux, z, counts, tokens, d = run(l, k, offsets, m, scoring, daux, dz)
+    status()
+    lh, mh = l.double().cpu().numpy(), None if m is None else m.cpu().numpy().astype(bool)
+    ra, rz, rc, rt = D.loss(lh, k, cuts, mh, scoring)
+    np.testing.assert_array_equal(tokens.cpu().numpy(), rt)
+    np.testing.assert_array_equal(counts.cpu().numpy(), rc)
+    fin = lh[np.isfinite(lh)]
+    spread = 0.0 if fin.size == 0 else float(min(fin.max(), 60) - max(fin.min(), -60))
+    # a score: (16 + 4 spread) units; at most 64 fp32 additions in a tile, the tiles in 64 bits
+    e = (80 + 4 * spread) * D.ULP
+    assert (np.abs(aux.cpu().numpy() - ra) <= e * np.abs(ra) + 1e-37).all()
+    assert (np.abs(z.cpu().numpy() - rz) <= 2 * e * (rz + np.sqrt(rz)) + 1e-12).all()
+    rd, tol = D.gradient(lh, k, cuts, mh, scoring, daux.double().cpu().numpy(), dz.double().cpu().numpy())
+    err = np.abs(d.cpu().numpy() - rd)
+    assert (err <= tol).all(), (err / tol).max()
+
+
+CASES = [  # T, E, k, cuts
+    (1, 1, 1, [0, 1]),
+    (1, 8, 2, [0, 1]),
+    (7, 3, 3, [0, 3, 3, 7]),
+    (33, 8, 2, [0, 1, 32, 33]),
+    (100, 9, 3, [0, 0, 50, 100, 100]),
+    (64, 16, 4, [5, 20, 60]),                       # tokens of no sequence at both ends
+    (300, 31, 8, [0, 31, 64, 65, 128, 300]),
+    (513, 60, 6, [0, 512, 513]),
+    (257, 64, 1, [0, 257]),
+    (200, 100, 4, list(range(0, 201, 5))),          # many short sequences in a tile
+    (1000, 128, 8, [0, 999, 1000]),
+    (130, 129, 2, [0, 64, 130]),
+    (700, 255, 8, [0, 100, 400, 700]),
+    (96, 256, 5, [0, 32, 64, 96]),
+    (40000, 8, 2, [0, 12345, 40000]),               # several tiles a sequence
+    (60000, 33, 4, [3, 30, 59990]),
+]
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,cuts", CASES)
+@pytest.mark.parametrize("dtype,mask,minus_inf", [(F32, False, False), (BF, True, False), (F32, True, True),
+                                                  (BF, False, True)])
+def test_losses_and_gradient_match_64_bits(T, E, k, cuts, scoring, dtype, mask, minus_inf):
+    l, m = make(T, E, T + E, dtype, mask, minus_inf)
+    check(l, k, cuts, m, scoring)
+
+
+def test_far_logits_neither_overflow_nor_vanish():
+    """Sigmoid scores far below zero: their ratio is still the exponential's."""
+    for shift in (-300.0, 80.0):
+        l = torch.randn((50, 12), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)) + shift
+        aux, z, counts, tokens, d = run(l, 3, None, None, "sigmoid", torch.ones(1, device="cuda"), None)
+        lh = l.double().cpu().numpy()
+        ra, rz, rc, rt = D.loss(lh, 3, [0, 50], None, "sigmoid")
+        rd, tol = D.gradient(lh, 3, [0, 50], None, "sigmoid", [1.0], [0.0])
+        # logits of this size carry 2^-16 of absolute rounding into every difference of two
+        assert abs(aux.item() - ra[0]) <= 1e-4 * ra[0] and abs(z.item() - rz[0]) <= 1e-5 * rz[0]
+        np.testing.assert_array_equal(counts.cpu().numpy(), rc)
+        assert torch.isfinite(d).all()
+        if shift < 0:  # (above, sigmoid(-l) of the logits leaves nothing)
+            scale = np.abs(rd).max()
+            assert np.abs(d.cpu().numpy() - rd).max() <= 1e-4 * scale
+
+
+def test_ties_go_to_the_lower_index():
+    l = torch.zeros((40, 20), device="cuda")
+    l[:, 7] = 1.0
+    aux, z, counts, tokens = router_balance(l, 3)
+    expect = torch.zeros((1, 20), dtype=torch.int32, device="cuda")
+    expect[0, [0, 1, 7]] = 40
+    assert torch.equal(counts, expect) and tokens.item() == 40
+
+
+def test_nothing_to_count():
+    l, _ = make(10, 6, 3, F32, False, False)
+    off = torch.tensor([0, 10], dtype=torch.int32, device="cuda")
+    one = torch.ones(1, device="cuda")
+    for logits, m in ((l, torch.zeros(10, dtype=torch.bool, device="cuda")), (torch.full_like(l, float("-inf")), None)):
+        aux, z, counts, tokens, d = run(logits, 2, off, m, "softmax", one, one)
+        assert aux.item() == 0 and z.item() == 0 and tokens.item() == 0 and not counts.any() and not d.any()
+    e = torch.empty((0, 6), device="cuda")
+    aux, z, counts, tokens, d = run(e, 2, None, None, "softmax", one, one)
+    assert aux.item() == 0 and z.item() == 0 and tokens.item() == 0 and d.shape == (0, 6)
+    aux, z, counts, tokens, d = run(l, 2, torch.zeros(1, dtype=torch.int32, device="cuda"), None, "softmax", one[:0], one[:0])
+    assert aux.shape == (0,) and counts.shape == (0, 6) and not d.any()
+
+
+def test_a_logit_that_is_nan_shows():
+    l, _ = make(64, 8, 4, F32, False, False)
+    off = torch.tensor([0, 30, 64], dtype=torch.int32, device="cuda")
+    l[40, 2] = float("nan")
+    one = torch.ones(2, device="cuda")
+    aux, z, counts, tokens, d = run(l, 2, off, None, "softmax", one, one)
+    assert torch.isfinite(aux[0]) and torch.isnan(aux[1]) and torch.isnan(z[1])
+    assert torch.isnan(d[40]).all() and torch.isfinite(d[:30]).all()
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_gradient_matches_differences(scoring):
+    """Central differences of the definition, the choices held fixed."""
+    T, E, k, cuts = 12, 5, 2, [0, 4, 9, 12]
+    l, _ = make(T, E, 8, F32, False, False)
+    lh = l.double().cpu().numpy()
+    hot = D.choices(lh, k)
+    daux, dz = np.array([1.0, -0.5, 2.0]), np.array([0.3, 1.0, -0.2])
+    *_, d = run(l, k, torch.tensor(cuts, dtype=torch.int32, device="cuda"), None, scoring,
+                torch.tensor(daux, dtype=F32, device="cuda"), torch.tensor(dz, dtype=F32, device="cuda"))
+    h, num = 1e-5, np.zeros((T, E))
+    for t in range(T):
+        for e in range(E):
+            v = []
+            for s in (h, -h):
+                x = lh.copy()
+                x[t, e] += s
+                a, z, *_ = D.loss(x, k, cuts, None, scoring, hot)
+                v.append((daux * a).sum() + (dz * z).sum())
+            num[t, e] = (v[0] - v[1]) / (2 * h)
+    assert np.abs(d.cpu().numpy() - num).max() <= 2e-5 * np.abs(num).max()
+
+
+def test_same_inputs_give_the_same_bits():
+    l, m = make(30000, 100, 5, BF, True, False)
+    off = torch.tensor([0, 100, 20000, 30000], dtype=torch.int32, device="cuda")
+    g = torch.ones(3, device="cuda")
+    first = run(l, 4, off, m, "softmax", g, g)
+    for _ in range(3):
+        for a, b in zip(first, run(l, 4, off, m, "softmax", g, g)):
+            assert torch.equal(a, b)
+
+
+def test_with_the_layer():
+    """One sequence without padding is the layer's own batch: the losses are those
+    that it reports, and with one choice a token the gradient through
+    backward(dlogits=...) is the one of its own coefficients."""
+    w = Workload("balance_layer", T=200, d=64, E=8, k=1, d_ff=128, act=ACT_RELU, gate=GATE_SWITCH, capacity_factor=1.0,
+                 dtype=DTYPE_BF16, bias="normal", dyadic=True, seed=77)
+    inp = make_inputs(w, device="cuda")
+    layer = layer_for(w)
+    args = [inp[n] for n in ("x", "W_r", "b_r", "W1", "W3", "W2")]
+    dbg = layer.debug_buffers(w.T, "cuda")
+    y, counts, dropped, aux, z = layer(*args, debug=dbg)
+    logits = dbg["logits_out"]
+    a, zz, c, n = router_balance(logits, w.k)
+    assert n.item() == w.T and torch.equal(c[0], counts)
+    assert abs(a.item() - aux.item()) <= 1e-5 * aux.item() and abs(zz.item() - z.item()) <= 1e-5 * z.item()
+    assert abs(a.item() - layer.balance_losses(w.T)[0].item()) <= 1e-5 * aux.item()
+    dy = torch.randn((w.T, w.d), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).to(BF)
+    own = layer.backward(*args, dy, aux_coef=0.5, z_coef=0.25)
+    dl = router_balance_backward(logits, c, n, torch.full((1,), 0.5, device="cuda"),
+                                 torch.full((1,), 0.25, device="cuda"), w.k)
+    ours = layer.backward(*args, dy, dlogits=dl)
+    without = layer.backward(*args, dy)
+    status()
+    for name in ("dx", "dW_r", "db_r"):
+        scale = own[name].abs().max()
+        assert (own[name] - ours[name]).abs().max() <= 2e-5 * scale, name
+        assert (own[name] - without[name]).abs().max() > 1e-3 * scale, name  # the losses do reach it
+    for name in ("dW1", "dW2"):
+        assert torch.equal(own[name], ours[name])
