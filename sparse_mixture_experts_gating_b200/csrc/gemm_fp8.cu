@@ -12,11 +12,12 @@
 // k-block's MMAs take 512 cycles at the tensor cores' rate, its read-back and
 // promotion 128 columns for each of the eight epilogue warps.
 //
-// Warp roles (320 threads, one CTA per SM):
+// Warp roles (384 threads, one CTA per SM):
 //   warp 0       TMA producer
 //   warp 1       TMEM allocator; lane 0 issues tcgen05.mma
-//   warps 2..9   promotion and epilogue: warp w owns TMEM lanes 32 (w % 4) ..
-//                (rows of the tile) and the columns of half (w - 2) / 4
+//   warps 2, 3   none (they complete the warpgroup that gives its registers away)
+//   warps 4..11  promotion and epilogue: warp w owns TMEM lanes 32 (w % 4) ..
+//                (rows of the tile) and the columns of half (w - 4) / 4
 // Pipelines: a ring of shared-memory stages (full / empty) and two TMEM
 // accumulators of 256 columns (tfull / tempty), one k-block each.  Every wait
 // is bounded; one that runs out records MOE_ERR_TIMEOUT, raises the CTA's
@@ -42,7 +43,11 @@ constexpr int BK = 128;                 // e4m3 elements per 128-byte shared-mem
 constexpr int MMA_N = 256;
 constexpr int B_HALF = 128 * BK;        // 16 KB per 128 rows of B
 constexpr int MAX_STAGES = 6;
-constexpr int NUM_THREADS = 320;
+constexpr int NUM_THREADS = 384;
+// 384 threads start with 168 registers each; the first warpgroup gives most of
+// its share to the two that hold the fp32 sums: 40 + 2 x 232 = 3 x 168.
+constexpr int REGS_START = 168, REGS_FEED = 40, REGS_SUM = 232;
+static_assert(REGS_FEED + 2 * REGS_SUM <= 3 * REGS_START, "the registers of the launch");
 constexpr int EPI_WARPS = 8;
 constexpr uint32_t TMEM_COLS = 2 * MMA_N;
 constexpr int ROW_STAGE = 80;           // bytes per staged output row: 64 + 16 of padding
@@ -181,6 +186,53 @@ __device__ __forceinline__ bool item_at(const Ctl* c, const Fp8Params& p, int64_
   return true;
 }
 
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Waits for the warp's TMEM loads; t passes through, so that no use of it moves up.
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&t)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(t[0]), "+r"(t[1]), "+r"(t[2]), "+r"(t[3]), "+r"(t[4]), "+r"(t[5]), "+r"(t[6]), "+r"(t[7]),
+                 "+r"(t[8]), "+r"(t[9]), "+r"(t[10]), "+r"(t[11]), "+r"(t[12]), "+r"(t[13]), "+r"(t[14]), "+r"(t[15]),
+                 "+r"(t[16]), "+r"(t[17]), "+r"(t[18]), "+r"(t[19]), "+r"(t[20]), "+r"(t[21]), "+r"(t[22]), "+r"(t[23]),
+                 "+r"(t[24]), "+r"(t[25]), "+r"(t[26]), "+r"(t[27]), "+r"(t[28]), "+r"(t[29]), "+r"(t[30]), "+r"(t[31])
+               :
+               : "memory");
+}
+
+// d = a * b + d on two fp32 numbers at once.
+__device__ __forceinline__ void fma2(float& d0, float& d1, uint32_t a0, uint32_t a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%0, %1};\n\t"
+      "fma.rn.f32x2 z, x, y, z;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}\n"
+      : "+f"(d0), "+f"(d1)
+      : "r"(a0), "r"(a1), "f"(b0), "f"(b1));
+}
+
+// acc[i] += t[i] * (a scale): one scale for all 32 columns, or (SB1) one for each in `b`.
+template <bool SB1>
+__device__ __forceinline__ void promote32(float* acc, const uint32_t (&t)[32], float s, const float* b) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    float s0 = s, s1 = s, s2 = s, s3 = s;
+    if (SB1) {
+      const float4 v = *reinterpret_cast<const float4*>(b + i);
+      s0 *= v.x; s1 *= v.y; s2 *= v.z; s3 *= v.w;
+    }
+    fma2(acc[i], acc[i + 1], t[i], t[i + 1], s0, s1);
+    fma2(acc[i + 2], acc[i + 3], t[i + 2], t[i + 3], s2, s3);
+  }
+}
+
 __device__ __forceinline__ float silu_mul(float a, float b) { return __fdividef(a, 1.f + __expf(-a)) * b; }
 
 template <int EPI, int AR, bool SB1>
@@ -217,6 +269,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tmem_base = ctl->tmem_slot;
   Item w;
 
+  if (warp < 4) {
+    reg_dec<REGS_FEED>();
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -274,11 +328,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       umma_commit(&ctl->drain);
       mbar_wait(&ctl->drain, 0, p.limit_ns);
     }
+  }
   } else {
     // ------------------------------------------------------------ promotion and epilogue
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    reg_inc<REGS_SUM>();
+    const int q = warp & 3, half = (warp - 4) >> 2;
     const int r_in_tile = q * 32 + lane;
-    uint8_t* stg = ctl->stage_out[warp - 2];
+    uint8_t* stg = ctl->stage_out[warp - 4];
     // PAIR: columns [64 half, +64) of W1, then of W3; else columns [128 half, +128)
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t col0 = PAIR ? 64u * half : 128u * half, col2 = PAIR ? 128u + 64u * half : 128u * half + 64u;
@@ -296,18 +352,31 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const float* sa = p.sa + (vrow ? static_cast<int64_t>(row) : 0) * p.sa_ld;
       const float* sb0 = p.sb0 + w.g * p.sb_gs + (SB1 ? 0 : static_cast<int64_t>(nb) * p.num_kb);
       const float* sb1 = PAIR ? p.sb1 + w.g * p.sb_gs + static_cast<int64_t>(nb) * p.num_kb : nullptr;
-      const int my_n = w.nt * 256 + half * 128 + (threadIdx.x - 64 - half * 128);  // SB1: the column this thread fetches
+      const int my_n = w.nt * 256 + half * 128 + (threadIdx.x - 128 - half * 128);  // SB1: the column this thread fetches
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      // The scales of a k-block are fetched two blocks ahead.
+      auto scale_a = [&](int kb) { return vrow && kb < w.kb1 ? __ldg(sa + kb) : 0.f; };
+      auto scale_b0 = [&](int kb) { return !SB1 && kb < w.kb1 ? __ldg(sb0 + kb) : 1.f; };
+      auto scale_b1 = [&](int kb) { return PAIR && kb < w.kb1 ? __ldg(sb1 + kb) : 1.f; };
+      auto scale_bc = [&](int kb) {
+        return SB1 && kb < w.kb1 && my_n < p.N ? __ldg(sb0 + static_cast<int64_t>(my_n) * p.num_kb + kb) : 0.f;
+      };
+      float a0 = scale_a(w.kb0), a1 = scale_a(w.kb0 + 1), b0 = scale_b0(w.kb0), b1 = scale_b0(w.kb0 + 1);
+      float c0 = scale_b1(w.kb0), c1 = scale_b1(w.kb0 + 1), n0_ = scale_bc(w.kb0), n1_ = scale_bc(w.kb0 + 1);
 #pragma unroll 1
       for (int kb = w.kb0; kb < w.kb1; ++kb) {
-        const float s_a = vrow ? __ldg(sa + kb) : 0.f;
-        const float s0 = SB1 ? s_a : s_a * __ldg(sb0 + kb);
-        const float s1 = PAIR ? s_a * __ldg(sb1 + kb) : s0;
+        const float s0 = a0 * b0, s1 = PAIR ? a0 * c0 : s0;
+        a0 = a1; b0 = b1; c0 = c1;
+        a1 = scale_a(kb + 2);
+        b1 = scale_b0(kb + 2);
+        c1 = scale_b1(kb + 2);
         float* sbs = ctl->sb[half][acc_i];  // (turns with the accumulator: the last block's may still be read)
         if (SB1) {  // this half's 128 scales of B, one per thread
-          sbs[threadIdx.x - 64 - half * 128] = my_n < p.N ? __ldg(sb0 + static_cast<int64_t>(my_n) * p.num_kb + kb) : 0.f;
+          sbs[threadIdx.x - 128 - half * 128] = n0_;
+          n0_ = n1_;
+          n1_ = scale_bc(kb + 2);
           named_barrier(1 + half, 128);
         }
         ok = ok && __all_sync(0xffffffffu,
@@ -315,31 +384,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (ok) {
           tc_fence_after();
           if (warp_live) {
+            // each load of 32 columns is in flight while the 32 before are added
             const uint32_t tb = lane_base + static_cast<uint32_t>(acc_i * MMA_N);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t t[32];
-              tmem_ld32(tb + (c < 2 ? col0 + c * 32 : col2 + (c - 2) * 32), t);
-              tmem_ld_wait();
-              if (SB1) {
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                  const float4 b = *reinterpret_cast<const float4*>(sbs + c * 32 + i);
-                  acc[c * 32 + i] = fmaf(__uint_as_float(t[i]), s0 * b.x, acc[c * 32 + i]);
-                  acc[c * 32 + i + 1] = fmaf(__uint_as_float(t[i + 1]), s0 * b.y, acc[c * 32 + i + 1]);
-                  acc[c * 32 + i + 2] = fmaf(__uint_as_float(t[i + 2]), s0 * b.z, acc[c * 32 + i + 2]);
-                  acc[c * 32 + i + 3] = fmaf(__uint_as_float(t[i + 3]), s0 * b.w, acc[c * 32 + i + 3]);
-                }
-              } else {
-                const float s = c < 2 ? s0 : s1;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(__uint_as_float(t[i]), s, acc[c * 32 + i]);
-              }
-            }
+            uint32_t t[32], v[32];
+            tmem_ld32(tb + col0, t);
+            tmem_ld_wait32(t);
+            tmem_ld32(tb + col0 + 32, v);
+            promote32<SB1>(acc, t, s0, sbs);
+            tmem_ld_wait32(v);
+            tmem_ld32(tb + col2, t);
+            promote32<SB1>(acc + 32, v, s0, sbs + 32);
+            tmem_ld_wait32(t);
+            tmem_ld32(tb + col2 + 32, v);
+            promote32<SB1>(acc + 64, t, s1, sbs + 64);
+            tmem_ld_wait32(v);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->tempty[acc_i]);
+            promote32<SB1>(acc + 96, v, s1, sbs + 96);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->tempty[acc_i]);
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->tempty[acc_i]);
         }
         if (++acc_i == 2) { acc_i = 0; acc_phase ^= 1u; }
         if (!ok && !SB1) break;
