@@ -32,7 +32,9 @@ cudaError_t launch_quantize_fp8(const QuantFp8Args& a, cudaStream_t s);
 // by row_gate[r], and with ksplit > 1 writes one partial per K range.
 // FP8_SWIGLU / FP8_RELU: the activation of the product(s), quantised to e4m3
 // with a scale for each 128 columns of a row.
-enum Fp8Epi { FP8_BF16 = 0, FP8_F32 = 1, FP8_SWIGLU = 2, FP8_RELU = 3 };
+// FP8_PAIR_F32: the two products of a SwiGLU layer as they are, W3's
+// pair_stride elements behind W1's (one partial per K range).
+enum Fp8Epi { FP8_BF16 = 0, FP8_F32 = 1, FP8_SWIGLU = 2, FP8_RELU = 3, FP8_PAIR_F32 = 4 };
 
 struct Fp8Args {
   int epi;
@@ -54,6 +56,7 @@ struct Fp8Args {
   float* out_scales;       // activations: [a_rows][ceil(N / 128)]
   int ksplit;
   int64_t split_stride;    // elements between the partials of consecutive K ranges
+  int64_t pair_stride;     // FP8_PAIR_F32
   const float* row_gate;   // FP8_F32: may be NULL
   const int32_t* offsets;  // [G + 1] first row of each group; NULL: one group of all rows
   unsigned int* err;
@@ -67,7 +70,7 @@ struct Fp8Params {
   const float *sb0, *sb1;
   int64_t sb_gs;           // floats between the scales of consecutive groups
   void* out;
-  int64_t ld_out, split_stride;
+  int64_t ld_out, split_stride, pair_stride;
   float* out_scales;
   int vec_out;             // output rows can be written 16 bytes at a time
   const float* row_gate;
@@ -102,5 +105,19 @@ struct Fp8ReduceArgs {
   int G;
 };
 cudaError_t launch_fp8_reduce(const Fp8ReduceArgs& a, cudaStream_t s);
+
+// Codes and scales of the hidden activation of the first *total_rows (at most
+// `rows`) rows, from the partials [ksplit] of the first projection (FP8_F32,
+// or with pair_stride > 0 FP8_PAIR_F32).
+struct Fp8HiddenArgs {
+  const float* P;
+  int ksplit;
+  int64_t split_stride, pair_stride, rows;
+  int N;
+  const int32_t* total_rows;
+  uint8_t* H;   // [rows][N]
+  float* Hs;    // [rows][ceil(N / 128)]
+};
+cudaError_t launch_fp8_hidden(const Fp8HiddenArgs& a, int num_sms, cudaStream_t s);
 
 }  // namespace moe

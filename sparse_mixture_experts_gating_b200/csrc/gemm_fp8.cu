@@ -50,7 +50,7 @@ constexpr int REGS_START = 168, REGS_FEED = 40, REGS_SUM = 232;
 static_assert(REGS_FEED + 2 * REGS_SUM <= 3 * REGS_START, "the registers of the launch");
 constexpr int EPI_WARPS = 8;
 constexpr uint32_t TMEM_COLS = 2 * MMA_N;
-constexpr int ROW_STAGE = 80;           // bytes per staged output row: 64 + 16 of padding
+constexpr int ROW_STAGE = 64;           // bytes per staged output row
 
 // AR: rows of A a stage holds.  No group has more rows than max_group_rows, so
 // a small batch stages 32 or 64 and keeps more weight bytes in flight; the
@@ -77,6 +77,10 @@ struct Ctl {
   alignas(16) float sb[2][2][128];      // per-row scales of B: [column half][parity][column]
   alignas(16) uint8_t stage_out[EPI_WARPS][32 * ROW_STAGE];
 };
+
+// Byte offset of 16-byte piece v of staged row r: the pieces are permuted so that
+// eight rows written at one v, and two rows read at four, take all 32 banks.
+__device__ __forceinline__ int stage_at(int r, int v) { return r * ROW_STAGE + ((v ^ (r >> 1 & 3)) << 4); }
 
 template <int AR>
 constexpr size_t smem_bytes() {
@@ -239,7 +243,8 @@ template <int EPI, int AR, bool SB1>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
                     const __grid_constant__ CUtensorMap tmB1, const Fp8Params p) {
-  constexpr bool PAIR = EPI == FP8_SWIGLU;  // 128 columns of W1 and the same of W3
+  constexpr bool PAIR = EPI == FP8_SWIGLU || EPI == FP8_PAIR_F32;  // 128 columns of W1 and the same of W3
+  constexpr bool F32 = EPI == FP8_F32 || EPI == FP8_PAIR_F32;
   constexpr bool ACT = EPI == FP8_SWIGLU || EPI == FP8_RELU;
   constexpr uint32_t IDESC = idesc_e4m3_f32(BM, MMA_N);
   using G = Geo<AR>;
@@ -413,7 +418,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       // Where warps meet at barriers, they leave an aborted CTA together.
       if (SB1) ok = named_barrier_and(1 + half, 128, ok);
-      if (PAIR) ok = named_barrier_and(3, 256, ok);  // (the last tile's hmax has been read, too)
+      if (EPI == FP8_SWIGLU) ok = named_barrier_and(3, 256, ok);  // (the last tile's hmax has been read, too)
       if (ACT) {
         // activation, then codes with one scale for each 128 columns of a row
         constexpr int NV = PAIR ? 64 : 128;
@@ -447,28 +452,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // 64 bytes of every row at a time through shared memory, so that the
         // stores run along rows
         constexpr int ELT = EPI == FP8_BF16 ? 2 : 4, PER = 64 / ELT;
-        const float g = (EPI == FP8_F32 && p.row_gate != nullptr && vrow) ? p.row_gate[row] : 1.f;
-        const int n0 = w.nt * 256 + half * 128;
+        const float g = (F32 && p.row_gate != nullptr && vrow) ? p.row_gate[row] : 1.f;
+        const int n0 = PAIR ? w.nt * 128 + half * 64 : w.nt * 256 + half * 128;
         const int nrows = min(32, ctl->offsets[w.g + 1] - (ctl->offsets[w.g] + w.mt * BM + q * 32));
         const int64_t row_base = ctl->offsets[w.g] + w.mt * BM + q * 32;
         uint8_t* out = static_cast<uint8_t*>(p.out) + static_cast<int64_t>(w.ks) * p.split_stride * ELT;
 #pragma unroll
         for (int c = 0; c < 128 / PER; ++c) {
-          uint4* srow = reinterpret_cast<uint4*>(stg + lane * ROW_STAGE);
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
+            uint4& piece = *reinterpret_cast<uint4*>(stg + stage_at(lane, v));
             if (EPI == FP8_BF16) {
               const float* s = acc + c * PER + v * 8;
-              srow[v] = make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]),
+              piece = make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]),
                                    pack_bf16x2(s[6], s[7]));
             } else {
               const float* s = acc + c * PER + v * 4;
-              srow[v] = make_uint4(__float_as_uint(s[0] * g), __float_as_uint(s[1] * g), __float_as_uint(s[2] * g),
+              piece = make_uint4(__float_as_uint(s[0] * g), __float_as_uint(s[1] * g), __float_as_uint(s[2] * g),
                                    __float_as_uint(s[3] * g));
             }
           }
           __syncwarp();
-          const int col = n0 + c * PER;
+          const int col = n0 + (PAIR ? c % 4 : c) * PER;
+          if (PAIR && c == 4) out += p.pair_stride * ELT;  // W3's columns
           if (p.vec_out) {
             const int seg = lane & 3;
 #pragma unroll
@@ -476,19 +482,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               const int rr = (lane >> 2) + 8 * i;
               if (rr < nrows && col + seg * (16 / ELT) < p.N)
                 *reinterpret_cast<uint4*>(out + ((row_base + rr) * p.ld_out + col) * ELT + seg * 16) =
-                    *reinterpret_cast<const uint4*>(stg + rr * ROW_STAGE + seg * 16);
+                    *reinterpret_cast<const uint4*>(stg + stage_at(rr, seg));
             }
           } else {
 #pragma unroll 1
             for (int i = lane; i < 32 * PER; i += 32) {
-              const int rr = i / PER, cc = i % PER;
+              const int rr = i / PER, cc = i % PER, at = stage_at(rr, cc * ELT >> 4) + (cc * ELT & 15);
               if (rr < nrows && col + cc < p.N) {
                 if (EPI == FP8_BF16)
                   *reinterpret_cast<uint16_t*>(out + ((row_base + rr) * p.ld_out + col + cc) * ELT) =
-                      *reinterpret_cast<const uint16_t*>(stg + rr * ROW_STAGE + cc * 2);
+                      *reinterpret_cast<const uint16_t*>(stg + at);
                 else
                   *reinterpret_cast<float*>(out + ((row_base + rr) * p.ld_out + col + cc) * ELT) =
-                      *reinterpret_cast<const float*>(stg + rr * ROW_STAGE + cc * 4);
+                      *reinterpret_cast<const float*>(stg + at);
               }
             }
           }
@@ -507,13 +513,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 }
 
 // ---------------------------------------------------------------- partials
-template <bool BF16>
-__global__ void __launch_bounds__(256) fp8_reduce_kernel(const Fp8ReduceArgs a) {
+// Thread: four columns of a row (VEC: as one 16-byte access), every partial in
+// order; eight partials' loads in flight.
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(128) fp8_reduce_kernel(const Fp8ReduceArgs a) {
+  __shared__ int s_last;
   pdl_wait();
   pdl_trigger();
   int64_t r0 = 0, r1 = a.rows;
   if (a.offsets != nullptr) {  // as the product's kernel takes them: clamped, ascending
-    __shared__ int s_last;
     if (threadIdx.x == 0) s_last = 0;
     __syncthreads();
     for (int g = threadIdx.x; g <= a.G; g += blockDim.x)
@@ -522,14 +530,91 @@ __global__ void __launch_bounds__(256) fp8_reduce_kernel(const Fp8ReduceArgs a) 
     r0 = min(max(a.offsets[0], 0), static_cast<int>(a.rows));
     r1 = s_last;
   }
-  const int64_t n = (r1 - r0) * a.N, base = r0 * a.N;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    float v = 0.f;
-    for (int k = 0; k < a.ksplit; ++k) v += a.P[k * a.split_stride + base + i];
-    const int64_t r = (base + i) / a.N, c = (base + i) - r * a.N;
-    if (BF16) static_cast<__nv_bfloat16*>(a.out)[r * a.ld_out + c] = __float2bfloat16(v);
-    else static_cast<float*>(a.out)[r * a.ld_out + c] = v;
+  const int c0 = (blockIdx.x * 128 + threadIdx.x) * 4;
+  if (c0 >= a.N) return;
+  for (int64_t r = r0 + blockIdx.y; r < r1; r += gridDim.y) {
+    const float* src = a.P + r * a.N + c0;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k0 = 0; k0 < a.ksplit; k0 += 8) {
+      float4 q[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float* s = src + (k0 + u) * a.split_stride;
+        q[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k0 + u < a.ksplit) {
+          if (VEC) {
+            q[u] = *reinterpret_cast<const float4*>(s);
+          } else {
+            q[u].x = s[0];
+            if (c0 + 1 < a.N) q[u].y = s[1];
+            if (c0 + 2 < a.N) q[u].z = s[2];
+            if (c0 + 3 < a.N) q[u].w = s[3];
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) { v[0] += q[u].x; v[1] += q[u].y; v[2] += q[u].z; v[3] += q[u].w; }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (c0 + i < a.N) {
+        if (BF16) static_cast<__nv_bfloat16*>(a.out)[r * a.ld_out + c0 + i] = __float2bfloat16(v[i]);
+        else static_cast<float*>(a.out)[r * a.ld_out + c0 + i] = v[i];
+      }
+    }
+  }
+}
+
+// The hidden activation from a cut first projection: 16 lanes take 128 columns
+// of a row, eight each; the partials in order, then as the fused epilogue.
+template <bool PAIR>
+__global__ void __launch_bounds__(256) fp8_hidden_kernel(const Fp8HiddenArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int l = threadIdx.x & 15;
+  const int groups = (a.N + 127) >> 7;
+  const int rows = min(static_cast<int>(a.rows), *a.total_rows);
+  const int64_t items = static_cast<int64_t>(rows) * groups, step = static_cast<int64_t>(gridDim.x) * 16;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  for (int64_t i0 = first & ~int64_t{1}; i0 < items; i0 += step) {  // (both teams of a warp run every step)
+    const int64_t i = i0 + (first & 1);
+    const int64_t r = i < items ? i / groups : 0;
+    const int g = i < items ? static_cast<int>(i - r * groups) : 0;
+    const int c = g * 128 + l * 8;
+    const bool live = i < items && c < a.N;  // N is a multiple of 16
+    float v[8], u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = u[j] = 0.f;
+    if (live) {
+      const float* s = a.P + r * a.N + c;
+#pragma unroll 4
+      for (int k = 0; k < a.ksplit; ++k, s += a.split_stride) {
+        const float4 q0 = *reinterpret_cast<const float4*>(s), q1 = *reinterpret_cast<const float4*>(s + 4);
+        v[0] += q0.x; v[1] += q0.y; v[2] += q0.z; v[3] += q0.w;
+        v[4] += q1.x; v[5] += q1.y; v[6] += q1.z; v[7] += q1.w;
+        if (PAIR) {
+          const float4 w0 = *reinterpret_cast<const float4*>(s + a.pair_stride);
+          const float4 w1 = *reinterpret_cast<const float4*>(s + a.pair_stride + 4);
+          u[0] += w0.x; u[1] += w0.y; u[2] += w0.z; u[3] += w0.w;
+          u[4] += w1.x; u[5] += w1.y; u[6] += w1.z; u[7] += w1.w;
+        }
+      }
+    }
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = PAIR ? silu_mul(v[j], u[j]) : fmaxf(v[j], 0.f);
+      m = fmaxf(m, fabsf(v[j]));
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const Fp8Scale q = fp8_scale(m);
+    if (live) {
+      *reinterpret_cast<uint2*>(a.H + r * a.N + c) =
+          make_uint2(e4m3x4(v[0] * q.inv, v[1] * q.inv, v[2] * q.inv, v[3] * q.inv),
+                     e4m3x4(v[4] * q.inv, v[5] * q.inv, v[6] * q.inv, v[7] * q.inv));
+      if (l == 0) a.Hs[r * groups + g] = q.scale;
+    }
   }
 }
 
@@ -569,21 +654,31 @@ int fp8_ksplit(int64_t rows, int G, int N, int K) {
   const int64_t tiles = (g + (rows - g) / BM) * ((N + 255) / 256);
   const int64_t num_kb = (K + BK - 1) / BK;
   if (tiles <= 0 || tiles > 4 * kSplitTargetCtas) return 1;
-  // The cut whose longest CTA (ceil(units / SMs) ranges of `per` k-blocks) is
-  // shortest; more ranges only for a gain above 3 % (each adds fp32 partials).
-  int64_t best = 1, best_len = (tiles + kSplitTargetCtas - 1) / kSplitTargetCtas * num_kb;
+  // Time of a cut, in tenths of a k-block's: the longest CTA runs ceil(units /
+  // SMs) ranges of `per` k-blocks, each followed by an epilogue (5 k-blocks for
+  // a full tile; next to nothing for a few rows, whose weight stream goes on
+  // under it); every partial is written and read once more (a k-block's time
+  // moves 1.6 MB), and a cut product needs a second launch (8 k-blocks of the
+  // tensor cores' time, 3.5 of the weight stream's).  Rows count in powers of
+  // two, so that the choice is constant between them.
+  int64_t r2 = 1;
+  while (r2 < rows) r2 <<= 1;
+  const int64_t epi = r2 <= 64 ? 2 : 50;
+  const int64_t launch = r2 <= 64 ? 35 : 80;
+  int64_t best = 1, best_t = (tiles + kSplitTargetCtas - 1) / kSplitTargetCtas * (10 * num_kb + epi);
   for (int64_t ks = 2; ks <= num_kb / 2; ++ks) {
     const int64_t per = (num_kb + ks - 1) / ks;
     const int64_t ranges = (num_kb + per - 1) / per;
-    const int64_t len = (tiles * ranges + kSplitTargetCtas - 1) / kSplitTargetCtas * per;
-    if (len * 32 < best_len * 31) { best = ranges; best_len = len; }
+    const int64_t t = (tiles * ranges + kSplitTargetCtas - 1) / kSplitTargetCtas * (10 * per + epi) +
+                      r2 * N * ranges / 20000 + launch;
+    if (t * 32 < best_t * 31) { best = ranges; best_t = t; }
   }
   return static_cast<int>(best);
 }
 
 cudaError_t plan_fp8(const Fp8Args& g, Fp8Plan* pl, const char** why) {
   *why = nullptr;
-  const bool pair = g.epi == FP8_SWIGLU;
+  const bool pair = g.epi == FP8_SWIGLU || g.epi == FP8_PAIR_F32;
   pl->epi = g.epi;
   pl->sb1 = g.b_rows == 1;
   pl->ar = pl->sb1 ? 128 : g.max_group_rows <= 32 ? 32 : g.max_group_rows <= 64 ? 64 : 128;
@@ -603,7 +698,7 @@ cudaError_t plan_fp8(const Fp8Args& g, Fp8Plan* pl, const char** why) {
   p.bn = pair ? 128 : 256;
   p.n_tiles = (g.N + p.bn - 1) / p.bn;
   p.num_kb = (g.K + BK - 1) / BK;
-  p.ksplit = g.epi == FP8_F32 ? std::max(1, std::min(g.ksplit, p.num_kb)) : 1;
+  p.ksplit = g.epi == FP8_F32 || g.epi == FP8_PAIR_F32 ? std::max(1, std::min(g.ksplit, p.num_kb)) : 1;
   p.kb_per = (p.num_kb + p.ksplit - 1) / p.ksplit;
   p.a_rows = g.a_rows;
   p.sa = g.sa;
@@ -614,10 +709,12 @@ cudaError_t plan_fp8(const Fp8Args& g, Fp8Plan* pl, const char** why) {
   p.out = g.out;
   p.ld_out = g.ld_out;
   p.split_stride = g.split_stride;
+  p.pair_stride = g.pair_stride;
   p.out_scales = g.out_scales;
   const int elt = g.epi == FP8_BF16 ? 2 : 4;
   p.vec_out = ((reinterpret_cast<uintptr_t>(g.out) | static_cast<uintptr_t>(g.ld_out * elt) |
-                static_cast<uintptr_t>(static_cast<int64_t>(g.N) * elt) | static_cast<uintptr_t>(g.split_stride * elt)) & 15) == 0;
+                static_cast<uintptr_t>(static_cast<int64_t>(g.N) * elt) | static_cast<uintptr_t>(g.split_stride * elt) |
+                static_cast<uintptr_t>(g.pair_stride * elt)) & 15) == 0;
   p.row_gate = g.row_gate;
   p.offsets = g.offsets;
   p.err = g.err;
@@ -629,17 +726,29 @@ cudaError_t launch_fp8(const Fp8Plan& pl, int num_sms, cudaStream_t s) {
   switch (pl.epi) {
     case FP8_BF16: return launch_ar<FP8_BF16>(pl, num_sms, s);
     case FP8_F32: return launch_ar<FP8_F32>(pl, num_sms, s);
+    case FP8_PAIR_F32: return launch_ar<FP8_PAIR_F32>(pl, num_sms, s);
     case FP8_SWIGLU: return launch_ar<FP8_SWIGLU>(pl, num_sms, s);
     default: return launch_ar<FP8_RELU>(pl, num_sms, s);
   }
 }
 
 cudaError_t launch_fp8_reduce(const Fp8ReduceArgs& a, cudaStream_t s) {
-  const int64_t n = a.rows * a.N;
-  if (n <= 0) return cudaSuccess;
-  const int64_t blocks = std::min<int64_t>((n + 255) / 256, 148 * 8);
-  if (a.out_is_bf16) return launch_pdl(fp8_reduce_kernel<true>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a);
-  return launch_pdl(fp8_reduce_kernel<false>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a);
+  if (a.rows <= 0 || a.N <= 0) return cudaSuccess;
+  const dim3 grid(static_cast<unsigned>((a.N + 511) / 512), static_cast<unsigned>(std::min<int64_t>(a.rows, 65535)));
+  const bool vec = a.N % 4 == 0;  // (partials are 256-byte aligned and N floats apart)
+  if (a.out_is_bf16)
+    return vec ? launch_pdl(fp8_reduce_kernel<true, true>, grid, dim3(128), 0, s, a)
+               : launch_pdl(fp8_reduce_kernel<true, false>, grid, dim3(128), 0, s, a);
+  return vec ? launch_pdl(fp8_reduce_kernel<false, true>, grid, dim3(128), 0, s, a)
+             : launch_pdl(fp8_reduce_kernel<false, false>, grid, dim3(128), 0, s, a);
+}
+
+cudaError_t launch_fp8_hidden(const Fp8HiddenArgs& a, int num_sms, cudaStream_t s) {
+  const int64_t items = a.rows * ((a.N + 127) / 128);
+  if (items <= 0) return cudaSuccess;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((items + 15) / 16, num_sms * 8)));
+  return a.pair_stride > 0 ? launch_pdl(fp8_hidden_kernel<true>, grid, dim3(256), 0, s, a)
+                           : launch_pdl(fp8_hidden_kernel<false>, grid, dim3(256), 0, s, a);
 }
 
 }  // namespace moe

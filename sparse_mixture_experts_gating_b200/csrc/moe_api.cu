@@ -123,6 +123,13 @@ int64_t yp_rows_of(const moe_layer& L, int64_t s, Weights kind) {
   return need_yp_of(L, kind) ? ksplit_of(L, s, kind) * s : 0;
 }
 
+// K ranges of the 8-bit first projection of s rows (SwiGLU: W1 and W3 columns
+// side by side); above 1 it writes fp32 partials, which a launch of their own
+// turns into the hidden activation.
+int fp8_ksplit1(const moe_layer& L, int64_t s) {
+  return fp8_ksplit(s, L.E + L.n_shared, L.act == MOE_ACT_SWIGLU ? (L.d_ff + 127) / 128 * 256 : L.d_ff, L.d);
+}
+
 // A row of x in the 8-bit path: its codes, then one scale for each 128 of
 // them, in one row of `x_pitch` bytes that the dispatch copies as it is.
 int64_t fp8_x_pitch(const moe_layer& L) {
@@ -250,6 +257,19 @@ Layout make_layout(const moe_layer& L, int64_t T, Weights kind = W_NATIVE) {
   for (int64_t s = 1; s < w.s_max && s <= groups; ++s) yp_rows = std::max<int64_t>(yp_rows, yp_rows_of(L, s, kind));
   for (int64_t s = groups + 127; s < w.s_max && s <= groups + int64_t{kSplitMaxTiles} * 128; s += 128)
     yp_rows = std::max<int64_t>(yp_rows, yp_rows_of(L, s, kind));
+  int64_t p_rows = 0;  // rows of the 8-bit first projection's partials
+  if (fp8) {  // the 8-bit splits change with the tile bound, as above, and at powers of two
+    w.ks1 = fp8_ksplit1(L, w.s_max);
+    auto both = [&](int64_t s) {
+      yp_rows = std::max<int64_t>(yp_rows, yp_rows_of(L, s, kind));
+      const int64_t ks1 = fp8_ksplit1(L, s);
+      if (ks1 > 1) p_rows = std::max<int64_t>(p_rows, ks1 * s);
+    };
+    for (int64_t s = 1; s < w.s_max && s <= groups; ++s) both(s);
+    for (int64_t s = groups + 127; s < w.s_max && s <= groups + int64_t{kSplitMaxTiles} * 128; s += 128) both(s);
+    for (int64_t s = 1; s < w.s_max; s <<= 1) both(s);
+    both(w.s_max);
+  }
   if (w4) {  // the 4-bit split also changes at every 16 / 32 / 64 rows (n-tile sizes) up to two waves of tiles
     for (int64_t s = groups + 1; s < w.s_max && s <= groups + int64_t{2 * kSplitTargetCtas} * 64; ++s)
       yp_rows = std::max<int64_t>(yp_rows, yp_rows_of(L, s, kind));
@@ -260,8 +280,8 @@ Layout make_layout(const moe_layer& L, int64_t T, Weights kind = W_NATIVE) {
   // and the second projection's partials in Yp; sized for every batch up to
   // kW4SmallMaxT tokens, so sizes stay monotone in T.
   w.small = w4 && T <= kW4SmallMaxT;
-  w.ks1 = 1;
-  size_t p_bytes = 0;
+  if (!fp8) w.ks1 = 1;
+  size_t p_bytes = sizeof(float) * static_cast<size_t>(p_rows) * (L.act == MOE_ACT_SWIGLU ? 2 : 1) * L.d_ff;
   if (w4) {
     const size_t nq = L.act == MOE_ACT_SWIGLU ? 2 : 1;
     for (int64_t t = 1; t <= std::min<int64_t>(T, kW4SmallMaxT); ++t) {
@@ -684,10 +704,17 @@ int forward_impl(moe_handle h, int64_t T, const void* x, const float* W_r, const
     a1.out = ws + w.Hp;
     a1.ld_out = L.d_ff;
     a1.out_scales = reinterpret_cast<float*>(ws + w.Hs);
-    a1.ksplit = 1;
+    a1.ksplit = w.ks1;
+    if (w.ks1 > 1) {
+      a1.epi = L.act == MOE_ACT_SWIGLU ? FP8_PAIR_F32 : FP8_F32;
+      a1.out = ws + w.P;
+      a1.split_stride = static_cast<int64_t>(w.s_max) * L.d_ff;
+      a1.pair_stride = L.act == MOE_ACT_SWIGLU ? w.ks1 * a1.split_stride : 0;
+    }
     a1.offsets = r.offsets;
     a1.err = di->err;
     Fp8Args a2 = a1;
+    a2.pair_stride = 0;
     a2.epi = FP8_F32;
     a2.N = L.d;
     a2.K = L.d_ff;
@@ -836,6 +863,20 @@ int forward_impl(moe_handle h, int64_t T, const void* x, const float* W_r, const
                : tc ? launch_gemm_tc(plan1, di->num_sms, s) : launch_gemm_simt(g1, w.s_max, s);
   }
   if ((rc = check(ce, "gemm1")) != MOE_OK) return rc;
+  if (fp8 && w.ks1 > 1) {
+    Fp8HiddenArgs ha;
+    memset(&ha, 0, sizeof(ha));
+    ha.P = reinterpret_cast<const float*>(ws + w.P);
+    ha.ksplit = fplan1.p.ksplit;
+    ha.split_stride = fplan1.p.split_stride;
+    ha.pair_stride = fplan1.p.pair_stride;
+    ha.rows = w.s_max;
+    ha.N = L.d_ff;
+    ha.total_rows = r.offsets + (L.E + L.n_shared);
+    ha.H = ws + w.Hp;
+    ha.Hs = reinterpret_cast<float*>(ws + w.Hs);
+    if ((rc = check(launch_fp8_hidden(ha, di->num_sms, s), "hidden activation")) != MOE_OK) return rc;
+  }
   if (w.f16) {  // the fp16 image of W2, made while the first projection runs
     ce = launch_convert_f16(W2, ws + w.W2h, static_cast<int64_t>(L.E + L.n_shared) * L.d * L.d_ff, di->err,
                             di->num_sms, s);

@@ -21,44 +21,74 @@
 namespace moe {
 namespace {
 
-// Eight consecutive elements of a row from column c on, as fp32; columns past
-// K read as 0.  vec: the row's 16-byte pieces are aligned and c + 8 <= K.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, int c, int K, bool vec, float (&v)[8]) {
-  if (vec && c + 8 <= K) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p + c));
+// Eight consecutive elements of a row, as they are loaded.
+template <typename XT>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t w = i < 2 ? u.x : i < 4 ? u.y : i < 6 ? u.z : u.w;
+    return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+  }
+  __device__ __forceinline__ float amax() const {  // (exact on pairs: a maximum rounds nothing)
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    __nv_bfloat162 m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+    m[0] = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+    return fmaxf(__low2float(m[0]), __high2float(m[0]));
+  }
+};
+template <>
+struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ float at(int i) const {
+    return i == 0 ? a.x : i == 1 ? a.y : i == 2 ? a.z : i == 3 ? a.w : i == 4 ? b.x : i == 5 ? b.y : i == 6 ? b.z : b.w;
+  }
+  __device__ __forceinline__ float amax() const {
+    return fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))),
+                 fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))));
+  }
+};
+
+// Elements c .. c + 7 of row p; columns past K read as 0.  vec: the row's
+// 16-byte pieces are aligned.
+__device__ __forceinline__ Eight<__nv_bfloat16> load8(const __nv_bfloat16* p, int c, int K, bool vec) {
+  Eight<__nv_bfloat16> v;
+  if (vec && c + 8 <= K) {
+    v.u = __ldg(reinterpret_cast<const uint4*>(p + c));
+  } else {
+    uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      const uint32_t lo = c + 2 * i < K ? __bfloat16_as_ushort(p[c + 2 * i]) : 0u;
+      const uint32_t hi = c + 2 * i + 1 < K ? __bfloat16_as_ushort(p[c + 2 * i + 1]) : 0u;
+      w[i] = lo | hi << 16;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < K ? __bfloat162float(p[c + i]) : 0.f;
+    v.u = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  return v;
 }
-__device__ __forceinline__ void load8(const float* p, int c, int K, bool vec, float (&v)[8]) {
+__device__ __forceinline__ Eight<float> load8(const float* p, int c, int K, bool vec) {
+  Eight<float> v;
   if (vec && c + 8 <= K) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p + c));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p + c + 4));
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    v.a = __ldg(reinterpret_cast<const float4*>(p + c));
+    v.b = __ldg(reinterpret_cast<const float4*>(p + c + 4));
   } else {
+    float w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < K ? p[c + i] : 0.f;
+    for (int i = 0; i < 8; ++i) w[i] = c + i < K ? p[c + i] : 0.f;
+    v.a = make_float4(w[0], w[1], w[2], w[3]);
+    v.b = make_float4(w[4], w[5], w[6], w[7]);
   }
+  return v;
 }
 
-__device__ __forceinline__ float amax8(const float (&v)[8]) {
-  float m = fabsf(v[0]);
-#pragma unroll
-  for (int i = 1; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
-  return m;
-}
-
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
-  return make_uint2(e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                    e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+template <typename XT>
+__device__ __forceinline__ uint2 codes8(const Eight<XT>& v, float inv) {
+  return make_uint2(e4m3x4(v.at(0) * inv, v.at(1) * inv, v.at(2) * inv, v.at(3) * inv),
+                    e4m3x4(v.at(4) * inv, v.at(5) * inv, v.at(6) * inv, v.at(7) * inv));
 }
 
 // n <= 8 bytes of `c` to dst; vec: dst is 8-byte aligned.
@@ -72,35 +102,42 @@ __device__ __forceinline__ void store8(uint8_t* dst, uint2 c, int n, bool vec) {
   }
 }
 
-// Groups of 128 elements of a row: 16 lanes per group, 8 elements per lane.
-// Grid-stride over the R * ceil(K / 128) groups of every matrix.
+// Groups of 128 elements of a row: 16 lanes per group, 8 elements per lane,
+// UNROLL groups of a team of 16 lanes in flight at once (one load of 16 bytes
+// per lane keeps 32 KB in flight per SM, too few for HBM's latency).
+constexpr int UNROLL = 4;
+
 template <typename XT>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const QuantFp8Args a, int kb_n, int vec_in, int vec_out) {
   const int l = threadIdx.x & 15;
-  const int64_t teams = static_cast<int64_t>(gridDim.x) * 16;
-  const int64_t items = static_cast<int64_t>(a.G) * a.R * kb_n;
+  const uint32_t teams = gridDim.x * 16u;
+  const uint32_t items = static_cast<uint32_t>(a.G) * static_cast<uint32_t>(a.R) * static_cast<uint32_t>(kb_n);
   const XT* x = static_cast<const XT*>(a.x);
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
-  // every lane of a warp runs the same number of steps: the shuffles below need both its teams
-  for (int64_t i0 = first & ~int64_t{1}; i0 < items; i0 += teams) {
-    const int64_t i = i0 + (first & 1);
+  // every lane runs every step: the shuffles need both teams of a warp
+  Eight<XT> v[UNROLL];
+  int64_t dst[UNROLL], sc[UNROLL];
+  int left[UNROLL];  // elements from this lane's first one to the end of the row; 0: no group
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
+    const uint32_t i = blockIdx.x * 16u + (threadIdx.x >> 4) + static_cast<uint32_t>(u) * teams;
     const bool live = i < items;
-    const uint32_t ii = live ? static_cast<uint32_t>(i) : 0u;
-    const uint32_t row = ii / static_cast<uint32_t>(kb_n);
-    const int g = static_cast<int>(ii - row * static_cast<uint32_t>(kb_n));
-    const uint32_t mat = row / static_cast<uint32_t>(a.R), r = row - mat * static_cast<uint32_t>(a.R);
-    const int c = g * F8_GROUP + l * 8;
-    float v[8];
-    load8(x + static_cast<int64_t>(mat) * a.gsx + static_cast<int64_t>(r) * a.ldx, c, live ? a.K : 0, vec_in, v);
-    float m = amax8(v);
+    const uint32_t row = live ? i / static_cast<uint32_t>(kb_n) : 0u;
+    const uint32_t g = live ? i - row * static_cast<uint32_t>(kb_n) : 0u;
+    const uint32_t mat = a.G == 1 ? 0u : row / static_cast<uint32_t>(a.R), r = row - mat * static_cast<uint32_t>(a.R);
+    const int c = static_cast<int>(g) * F8_GROUP + l * 8;
+    left[u] = live ? a.K - c : 0;
+    dst[u] = static_cast<int64_t>(mat) * a.gsc + static_cast<int64_t>(r) * a.ldc + c;
+    sc[u] = static_cast<int64_t>(mat) * a.gss + static_cast<int64_t>(r) * a.lds + g;
+    v[u] = load8(x + static_cast<int64_t>(mat) * a.gsx + static_cast<int64_t>(r) * a.ldx, c, live ? a.K : 0, vec_in);
+  }
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
+    float m = v[u].amax();
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const Fp8Scale q = fp8_scale(m);
-    if (live) {
-      uint8_t* dst = a.codes + static_cast<int64_t>(mat) * a.gsc + static_cast<int64_t>(r) * a.ldc + c;
-      store8(dst, codes8(v, q.inv), a.K - c, vec_out);
-      if (l == 0) a.scales[static_cast<int64_t>(mat) * a.gss + static_cast<int64_t>(r) * a.lds + g] = q.scale;
-    }
+    store8(a.codes + dst[u], codes8(v[u], q.inv), left[u], vec_out);
+    if (l == 0 && left[u] > 0) a.scales[sc[u]] = q.scale;
   }
 }
 
@@ -120,17 +157,17 @@ __global__ void __launch_bounds__(256) quant_tile_kernel(const QuantFp8Args a, i
   const int kb = static_cast<int>(tile - static_cast<uint32_t>(rb) * static_cast<uint32_t>(kb_n));
   const XT* x = static_cast<const XT*>(a.x) + static_cast<int64_t>(mat) * a.gsx;
   const int c = kb * 128 + tx * 8;
-  float v[8][8];
+  Eight<XT> v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int r = rb * 128 + ty + 16 * j;
-    load8(x + static_cast<int64_t>(r) * a.ldx, c, r < a.R ? a.K : 0, vec_in, v[j]);
+    v[j] = load8(x + static_cast<int64_t>(r) * a.ldx, c, r < a.R ? a.K : 0, vec_in);
   }
   float inv[8];
   if (BLOCK) {
     float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, amax8(v[j]));
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, v[j].amax());
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = m;
@@ -145,9 +182,9 @@ __global__ void __launch_bounds__(256) quant_tile_kernel(const QuantFp8Args a, i
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float m = fabsf(v[0][i]);
+      float m = fabsf(v[0].at(i));
 #pragma unroll
-      for (int j = 1; j < 8; ++j) m = fmaxf(m, fabsf(v[j][i]));
+      for (int j = 1; j < 8; ++j) m = fmaxf(m, fabsf(v[j].at(i)));
       s_red[ty * 128 + tx * 8 + i] = m;
     }
     __syncthreads();
@@ -174,7 +211,7 @@ __global__ void __launch_bounds__(256) quant_tile_kernel(const QuantFp8Args a, i
     for (int i = 0; i < 8; ++i) {
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
-        const uint32_t w = e4m3x2(v[j][i] * inv[i], v[j + 1][i] * inv[i]);
+        const uint32_t w = e4m3x2(v[j].at(i) * inv[i], v[j + 1].at(i) * inv[i]);
         s_t[(tx * 8 + i) * 144 + ty + 16 * j] = static_cast<uint8_t>(w);
         s_t[(tx * 8 + i) * 144 + ty + 16 * (j + 1)] = static_cast<uint8_t>(w >> 8);
       }
@@ -199,9 +236,8 @@ cudaError_t launch_x(const QuantFp8Args& a, cudaStream_t s) {
   const int vec_out = ((reinterpret_cast<uintptr_t>(a.codes) | static_cast<uintptr_t>(a.ldc) |
                         static_cast<uintptr_t>(a.gsc)) & 7) == 0;
   if (a.block_rows == 1 && !a.transpose) {
-    const int64_t items = static_cast<int64_t>(a.G) * a.R * kb;
-    int64_t blocks = (items + 15) / 16;
-    if (blocks > 148 * 16) blocks = 148 * 16;
+    const int64_t items = static_cast<int64_t>(a.G) * a.R * kb;  // below 2^31
+    const int64_t blocks = (items + 16 * UNROLL - 1) / (16 * UNROLL);
     quant_rows_kernel<XT><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a, kb, vec_in, vec_out);
   } else {
     const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.G) * rb * kb);

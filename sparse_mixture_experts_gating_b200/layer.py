@@ -32,30 +32,44 @@ def _stream_handle(stream) -> int:
 
 
 @contextlib.contextmanager
-def _on(device, stream):
-    """Run on ``device`` and on ``stream`` (None: that device's current stream),
-    with torch's allocations on the same stream; yields the stream's handle."""
+def _switched(index: int, stream):
+    """``index``'s device current, and on ``stream`` if one is given (torch's
+    allocations too); yields the stream's handle."""
     with contextlib.ExitStack() as stack:
-        if device.index is not None and device.index != torch.cuda.current_device():
-            stack.enter_context(torch.cuda.device(device))
+        stack.enter_context(torch.cuda.device(index))
         if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+            if stream.device.index != index:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
             stack.enter_context(torch.cuda.stream(stream))
-        yield torch.cuda.current_stream(device).cuda_stream
+        yield torch._C._cuda_getCurrentRawStream(index)
+
+
+def _on(index: int, stream):
+    """A context that runs on the tensors' device and on ``stream`` (None: that
+    device's current stream) and yields the stream's handle."""
+    if stream is None and torch.cuda.current_device() == index:
+        return contextlib.nullcontext(torch._C._cuda_getCurrentRawStream(index))
+    return _switched(index, stream)
 
 
 def _blocks(n: int) -> int:
     return (n + 127) // 128
 
 
-def _check_tensor(name, t, device, dtypes, shape=None, contiguous=True):
-    """A device tensor of one of the dtypes, the shape and (by default) contiguous."""
-    if not isinstance(t, torch.Tensor) or t.device != device or device.type != "cuda":
-        raise ValueError(f"{name}: want a tensor on {device if device.type == 'cuda' else 'a CUDA device'}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: want {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+def _device_of(name, t) -> int:
+    """The index of the CUDA device that a tensor is on."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: want a tensor on a CUDA device")
+    return t.get_device()
+
+
+def _check_tensor(name, t, index, dtype, shape=None, contiguous=True):
+    """A tensor on CUDA device ``index`` of the dtype, the shape and (by default) contiguous."""
+    if _device_of(name, t) != index:
+        raise ValueError(f"{name}: want a tensor on cuda:{index}, got {t.device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: want {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: want shape {tuple(shape)}, got {tuple(t.shape)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name}: want a contiguous tensor")
@@ -198,31 +212,28 @@ class MoELayer:
         hidden activation are quantised on the way.  Returns like forward().
         Without ``workspace`` every call takes its own from torch's allocator,
         so calls on several streams or in several captured graphs share none."""
-        T, dev = x.shape[0], x.device
-        G = self.E + self.n_shared
-        _check_tensor("x", x, dev, (torch.bfloat16,), (T, self.d))
-        _check_tensor("W_r", W_r, dev, (torch.float32,), (self.E, self.d))
+        dev, T, G = _device_of("x", x), x.shape[0], self.E + self.n_shared
+        _check_tensor("x", x, dev, torch.bfloat16, (T, self.d))
+        _check_tensor("W_r", W_r, dev, torch.float32, (self.E, self.d))
         if b_r is not None:
-            _check_tensor("b_r", b_r, dev, (torch.float32,), (self.E,))
+            _check_tensor("b_r", b_r, dev, torch.float32, (self.E,))
         for name, q, rows, cols in (("W1q", W1q, self.d_ff, self.d), ("W3q", W3q, self.d_ff, self.d),
                                     ("W2q", W2q, self.d, self.d_ff)):
             if q is not None:
-                _check_tensor(name + " codes", q[0], dev, (FP8,), (G, rows, cols))
-                _check_tensor(name + " scales", q[1], dev, (torch.float32,), (G, _blocks(rows), _blocks(cols)))
-        if W1q is None or W2q is None:
-            raise ValueError("forward_fp8: W1q and W2q are (codes, scales) pairs")
+                _check_tensor(name + " codes", q[0], dev, FP8, (G, rows, cols))
+                _check_tensor(name + " scales", q[1], dev, torch.float32, (G, _blocks(rows), _blocks(cols)))
+            elif name != "W3q":
+                raise ValueError(f"forward_fp8: {name} is a (codes, scales) pair")
         if out is not None:
-            _check_tensor("out", out, dev, (torch.bfloat16,), (T, self.d))
+            _check_tensor("out", out, dev, torch.bfloat16, (T, self.d))
         with _on(dev, stream) as handle:
-            y = out if out is not None else torch.empty((T, self.d), dtype=x.dtype, device=dev)
+            y = out if out is not None else torch.empty_like(x)
             if stats is None:
-                stats = (torch.empty(self.E, dtype=torch.int32, device=dev),
-                         torch.empty(1, dtype=torch.int32, device=dev),
-                         torch.empty(1, dtype=torch.float32, device=dev),
-                         torch.empty(1, dtype=torch.float32, device=dev))
+                stats = (W_r.new_empty(self.E, dtype=torch.int32), W_r.new_empty(1, dtype=torch.int32),
+                         W_r.new_empty(1), W_r.new_empty(1))
             counts, dropped, aux, z = stats
             if workspace is None:
-                workspace = torch.empty(max(self.workspace_bytes_fp8(T), 256), dtype=torch.uint8, device=dev)
+                workspace = W_r.new_empty(max(self.workspace_bytes_fp8(T), 256), dtype=torch.uint8)
                 self._last = workspace
             dbg = _debug_struct(debug, events, stream)
             q3, s3 = (None, None) if W3q is None else W3q
@@ -250,7 +261,7 @@ class MoELayer:
                 self._bw = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
             bw_workspace = self._bw
         if dlogits is not None:
-            _check_tensor("dlogits", dlogits, dev, (torch.float32,), (T, self.E))
+            _check_tensor("dlogits", dlogits, x.get_device(), torch.float32, (T, self.E))
         f32 = dict(dtype=torch.float32, device=dev)
         g = dict(grads or {})
         g.setdefault("dx", torch.empty((T, self.d), **f32))
@@ -309,12 +320,15 @@ def _rows_of(t: torch.Tensor):
     [rows][columns] laid out one after another, or None if it is not."""
     if t.dim() < 2 or t.stride(-1) != 1 and t.shape[-1] > 1:
         return None
+    if t.dim() == 2:
+        (rows, cols), ld = t.shape, t.stride(0)
+        if rows <= 1:  # one row: its stride says nothing
+            ld = (cols + 15) // 16 * 16
+        return (1, rows, cols, ld) if ld >= cols else None
     rows, cols = t.shape[-2:]
     ld = t.stride(-2) if rows > 1 else max(t.stride(-2), cols)
     if ld < cols:
         return None
-    if t.numel() == cols:  # one row: its stride says nothing
-        ld = (cols + 15) // 16 * 16
     mats, step = 1, rows * ld
     for n, s in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
         if n != 1 and s != step:
@@ -330,11 +344,10 @@ def quantize_fp8(x: torch.Tensor, *, block_rows: int = 1, transpose: bool = Fals
     transposed matrices [..., K, R].  The codes' rows start on 16-byte
     boundaries (a view of a wider tensor where the row length is no multiple
     of 16); scales are [..., ceil(rows / block_rows), ceil(columns / 128)]."""
-    dev = x.device
-    _check_tensor("x", x, dev, (torch.bfloat16, torch.float32), contiguous=False)
-    if x.dim() < 2:
-        raise ValueError("quantize_fp8: x needs at least two dimensions")
-    if block_rows not in (1, 128):
+    dev = _device_of("x", x)
+    if x.dim() < 2 or x.dtype not in DTYPE:
+        raise ValueError(f"quantize_fp8: x is bf16 or fp32 with at least two dimensions, got {x.dtype} {tuple(x.shape)}")
+    if block_rows != 1 and block_rows != 128:
         raise ValueError("quantize_fp8: block_rows must be 1 or 128")
     with _on(dev, stream) as handle:
         form = _rows_of(x)
@@ -344,11 +357,13 @@ def quantize_fp8(x: torch.Tensor, *, block_rows: int = 1, transpose: bool = Fals
         mats, R, K, ld = form
         rows, cols = (K, R) if transpose else (R, K)
         pitch = (cols + 15) // 16 * 16
-        codes = torch.empty(x.shape[:-2] + (rows, pitch), dtype=FP8, device=dev)[..., :cols]
-        scales = torch.empty(x.shape[:-2] + ((rows + block_rows - 1) // block_rows, _blocks(cols)),
-                             dtype=torch.float32, device=dev)
-        check(lib().moe_quantize_fp8(_ptr(x), DTYPE[x.dtype], mats, R, K, ld, block_rows, int(transpose), _ptr(codes),
-                                     pitch, _ptr(scales), handle))
+        lead = x.shape[:-2]
+        codes = x.new_empty(lead + (rows, pitch), dtype=FP8)
+        if pitch != cols:
+            codes = codes[..., :cols]
+        scales = x.new_empty(lead + ((rows + block_rows - 1) // block_rows, _blocks(cols)), dtype=torch.float32)
+        check(lib().moe_quantize_fp8(x.data_ptr(), DTYPE[x.dtype], mats, R, K, ld, block_rows, int(transpose),
+                                     codes.data_ptr(), pitch, scales.data_ptr(), handle))
     return codes, scales
 
 
@@ -359,58 +374,58 @@ def matmul_fp8(a, b, *, offsets: Optional[torch.Tensor] = None, out_dtype=torch.
     offsets[g + 1] - 1 of a are multiplied by b[g]; rows of no group are left as
     they were in ``out``.  Returns [M, N] in out_dtype (bf16 or fp32)."""
     (ac, sa), (bc, sb) = a, b
-    dev = ac.device
-    _check_tensor("a codes", ac, dev, (FP8,), contiguous=False)
-    _check_tensor("b codes", bc, dev, (FP8,), contiguous=False)
+    dev = _device_of("a codes", ac)
+    _check_tensor("a codes", ac, dev, FP8, contiguous=False)
+    _check_tensor("b codes", bc, dev, FP8, contiguous=False)
     if ac.dim() != 2 or bc.dim() != (2 if offsets is None else 3) or ac.shape[1] != bc.shape[-1]:
         raise ValueError(f"matmul_fp8: a [M, K] and b {'[N, K]' if offsets is None else '[G, N, K]'}, got "
                          f"{tuple(ac.shape)} and {tuple(bc.shape)}")
     M, K = ac.shape
-    N = bc.shape[-2]
-    G = 1 if offsets is None else bc.shape[0]
-    _check_tensor("a scales", sa, dev, (torch.float32,), (M, _blocks(K)))
-    lead = tuple(bc.shape[:-2])
-    if sb.dim() != bc.dim() or sb.shape[-2] not in (N, _blocks(N)):
-        raise ValueError(f"matmul_fp8: b scales have {N} or {_blocks(N)} rows, got {tuple(sb.shape)}")
-    b_rows = 128 if sb.shape[-2] == _blocks(N) else 1
-    _check_tensor("b scales", sb, dev, (torch.float32,), lead + (sb.shape[-2], _blocks(K)))
+    N, lead, kb = bc.shape[-2], bc.shape[:-2], _blocks(K)
+    G = 1 if offsets is None else lead[0]
+    _check_tensor("a scales", sa, dev, torch.float32, (M, kb))
+    b_rows = 1 if sb.dim() == bc.dim() and sb.shape[-2] == N and N > 1 else 128
+    _check_tensor("b scales", sb, dev, torch.float32, lead + (N if b_rows == 1 else _blocks(N), kb))
     if offsets is not None:
-        _check_tensor("offsets", offsets, dev, (torch.int32,), (G + 1,))
+        _check_tensor("offsets", offsets, dev, torch.int32, (G + 1,))
     if out_dtype not in DTYPE:
         raise ValueError(f"matmul_fp8: out_dtype is bf16 or fp32, got {out_dtype}")
     fa, fb = _rows_of(ac), _rows_of(bc)
     if fa is None or fb is None:
         raise ValueError("matmul_fp8: the codes' rows must be contiguous, their matrices one after another")
+    ld_out = N
     if out is not None:
-        _check_tensor("out", out, dev, (out_dtype,), (M, N), contiguous=False)
-        if _rows_of(out) is None:
+        _check_tensor("out", out, dev, out_dtype, (M, N), contiguous=False)
+        fo = _rows_of(out)
+        if fo is None:
             raise ValueError("matmul_fp8: out's rows must be contiguous")
+        ld_out = fo[3]
     with _on(dev, stream) as handle:
         if out is None:
-            out = torch.empty((M, N), dtype=out_dtype, device=dev)
-        n = int(lib().moe_matmul_fp8_workspace_bytes(M, N, K, G))
-        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-        check(lib().moe_matmul_fp8(M, N, K, G, _ptr(ac), fa[3], _ptr(sa), _ptr(bc), fb[3], _ptr(sb), b_rows,
-                                   _ptr(offsets), _ptr(out), DTYPE[out_dtype], _rows_of(out)[3], _ptr(ws), n, handle))
+            out = sa.new_empty((M, N), dtype=out_dtype)
+        L = lib()
+        n = L.moe_matmul_fp8_workspace_bytes(M, N, K, G)
+        ws = sa.new_empty(n, dtype=torch.uint8) if n else None
+        check(L.moe_matmul_fp8(M, N, K, G, ac.data_ptr(), fa[3], sa.data_ptr(), bc.data_ptr(), fb[3], sb.data_ptr(),
+                               b_rows, _ptr(offsets), out.data_ptr(), DTYPE[out_dtype], ld_out, _ptr(ws), n, handle))
     return out
 
 
 def _balance_args(name, logits, k, offsets, mask, scoring):
-    if logits.dim() != 2:
-        raise ValueError(f"{name}: logits are [T, E]")
-    dev = logits.device
-    _check_tensor("logits", logits, dev, (torch.float32, torch.bfloat16))
+    dev = _device_of("logits", logits)
+    if logits.dim() != 2 or logits.dtype not in DTYPE or not logits.is_contiguous():
+        raise ValueError(f"{name}: logits are [T, E], fp32 or bf16 and contiguous")
     if scoring not in SCORING:
         raise ValueError(f"{name}: scoring is one of {sorted(SCORING)}")
     T, E = logits.shape
     B = 1
     if offsets is not None:
-        if offsets.dim() != 1 or offsets.shape[0] < 1:
+        B = offsets.numel() - 1
+        if B < 0:
             raise ValueError(f"{name}: offsets are [sequences + 1]")
-        _check_tensor("offsets", offsets, dev, (torch.int32,))
-        B = offsets.shape[0] - 1
+        _check_tensor("offsets", offsets, dev, torch.int32, (B + 1,))
     if mask is not None:
-        _check_tensor("mask", mask, dev, (torch.bool, torch.uint8), (T,))
+        _check_tensor("mask", mask, dev, torch.uint8 if mask.dtype == torch.uint8 else torch.bool, (T,))
     return dev, T, E, B
 
 
@@ -424,14 +439,14 @@ def router_balance(logits: torch.Tensor, k: int, *, offsets: Optional[torch.Tens
     scoring: "softmax" or "sigmoid" (normalised over the experts)."""
     dev, T, E, B = _balance_args("router_balance", logits, k, offsets, mask, scoring)
     with _on(dev, stream) as handle:
-        aux, z = torch.empty((2, B), dtype=torch.float32, device=dev)
-        counts = torch.empty((B, E), dtype=torch.int32, device=dev)
-        tokens = torch.empty(B, dtype=torch.int32, device=dev)
-        n = int(lib().moe_router_balance_workspace_bytes(T, E, B))
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        check(lib().moe_router_balance(T, E, int(k), _ptr(logits), DTYPE[logits.dtype], SCORING[scoring], B,
-                                       _ptr(offsets), _ptr(mask), _ptr(aux), _ptr(z), _ptr(counts), _ptr(tokens),
-                                       _ptr(ws), n, handle))
+        aux, z = logits.new_empty(B, dtype=torch.float32), logits.new_empty(B, dtype=torch.float32)
+        counts, tokens = logits.new_empty((B, E), dtype=torch.int32), logits.new_empty(B, dtype=torch.int32)
+        L = lib()
+        n = L.moe_router_balance_workspace_bytes(T, E, B)
+        ws = logits.new_empty(n, dtype=torch.uint8)
+        check(L.moe_router_balance(T, E, k, logits.data_ptr(), DTYPE[logits.dtype], SCORING[scoring], B,
+                                   _ptr(offsets), _ptr(mask), aux.data_ptr(), z.data_ptr(), counts.data_ptr(),
+                                   tokens.data_ptr(), ws.data_ptr(), n, handle))
     return aux, z, counts, tokens
 
 
@@ -443,16 +458,16 @@ def router_balance_backward(logits: torch.Tensor, counts: torch.Tensor, tokens: 
     logits, from router_balance's counts and tokens (held fixed); daux and dz
     are [sequences] fp32 or None.  Zero for padding and tokens of no sequence."""
     dev, T, E, B = _balance_args("router_balance_backward", logits, k, offsets, mask, scoring)
-    _check_tensor("counts", counts, dev, (torch.int32,), (B, E))
-    _check_tensor("tokens", tokens, dev, (torch.int32,), (B,))
+    _check_tensor("counts", counts, dev, torch.int32, (B, E))
+    _check_tensor("tokens", tokens, dev, torch.int32, (B,))
     for name, g in (("daux", daux), ("dz", dz)):
         if g is not None:
-            _check_tensor(name, g, dev, (torch.float32,), (B,))
+            _check_tensor(name, g, dev, torch.float32, (B,))
     with _on(dev, stream) as handle:
-        dlogits = torch.empty((T, E), dtype=torch.float32, device=dev)
-        check(lib().moe_router_balance_backward(T, E, int(k), _ptr(logits), DTYPE[logits.dtype], SCORING[scoring], B,
-                                                _ptr(offsets), _ptr(mask), _ptr(counts), _ptr(tokens), _ptr(daux),
-                                                _ptr(dz), _ptr(dlogits), handle))
+        dlogits = logits.new_empty((T, E), dtype=torch.float32)
+        check(lib().moe_router_balance_backward(T, E, k, logits.data_ptr(), DTYPE[logits.dtype], SCORING[scoring], B,
+                                                _ptr(offsets), _ptr(mask), counts.data_ptr(), tokens.data_ptr(),
+                                                _ptr(daux), _ptr(dz), dlogits.data_ptr(), handle))
     return dlogits
 
 
