@@ -73,6 +73,7 @@ struct Fp8Params {
   int64_t ld_out, split_stride, pair_stride;
   float* out_scales;
   int vec_out;             // output rows can be written 16 bytes at a time
+  int tma_out;             // and whole tiles by TMA
   const float* row_gate;
   const int32_t* offsets;
   unsigned int* err;
@@ -80,7 +81,7 @@ struct Fp8Params {
 };
 
 struct Fp8Plan {
-  CUtensorMap a, b0, b1;
+  CUtensorMap a, b0, b1, out;
   Fp8Params p;
   int epi, ar, sb1;
 };

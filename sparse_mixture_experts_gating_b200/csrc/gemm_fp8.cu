@@ -14,8 +14,12 @@
 //
 // Warp roles (384 threads, one CTA per SM):
 //   warp 0       TMA producer
-//   warp 1       TMEM allocator; lane 0 issues tcgen05.mma
-//   warps 2, 3   none (they complete the warpgroup that gives its registers away)
+//   warps 1, 2   lane 0 of each issues the tcgen05.mma of every other k-block:
+//                the issue of a k-block's MMAs returns when they are nearly
+//                done, so one thread alone would leave the tensor core idle
+//                while it waits for the next block's barriers (warp 1 also
+//                allocates TMEM)
+//   warp 3       none (it completes the warpgroup that gives its registers away)
 //   warps 4..11  promotion and epilogue: warp w owns TMEM lanes 32 (w % 4) ..
 //                (rows of the tile) and the columns of half (w - 4) / 4
 // Pipelines: a ring of shared-memory stages (full / empty) and two TMEM
@@ -50,17 +54,26 @@ constexpr int REGS_START = 168, REGS_FEED = 40, REGS_SUM = 232;
 static_assert(REGS_FEED + 2 * REGS_SUM <= 3 * REGS_START, "the registers of the launch");
 constexpr int EPI_WARPS = 8;
 constexpr uint32_t TMEM_COLS = 2 * MMA_N;
-constexpr int ROW_STAGE = 64;           // bytes per staged output row
+constexpr int ROW_STAGE = 64;           // bytes per staged output row of a warp's own stores
+constexpr int OUT_HALF = 2 * 16384;     // two boxes of 128 rows x 128 bytes of a warpgroup's TMA stores
 
 // AR: rows of A a stage holds.  No group has more rows than max_group_rows, so
 // a small batch stages 32 or 64 and keeps more weight bytes in flight; the
 // M = 128 MMA then reads the bytes that follow, which only feed accumulator
 // rows that are never stored.
+//
+// OUT_BYTES: where the summing warps lay out what they store.  With whole
+// tiles (AR 128) a warpgroup lays out 128 rows x 256 bytes and stores them by
+// TMA under the next tile's products: stored by the threads themselves, every
+// CTA's tile at the same time, a tile's 64 KB took 6200 cycles of 32000.  That
+// leaves room for three stages instead of four.
 template <int AR>
 struct Geo {
   static constexpr int A_ST = AR * BK;
   static constexpr int STAGE_BYTES = A_ST + 2 * B_HALF;
-  static constexpr int STAGES = (196 * 1024 / STAGE_BYTES) < MAX_STAGES ? (196 * 1024 / STAGE_BYTES) : MAX_STAGES;
+  static constexpr int OUT_BYTES = AR == BM ? 2 * OUT_HALF : EPI_WARPS * 32 * ROW_STAGE;
+  static constexpr int ROOM = 226 * 1024 - 6 * 1024 - OUT_BYTES;
+  static constexpr int STAGES = (ROOM / STAGE_BYTES) < MAX_STAGES ? (ROOM / STAGE_BYTES) : MAX_STAGES;
 };
 
 struct Ctl {
@@ -68,14 +81,13 @@ struct Ctl {
   uint64_t empty[MAX_STAGES];
   uint64_t tfull[2];
   uint64_t tempty[2];
-  uint64_t drain;
+  uint64_t drain[2];
   uint32_t tmem_slot;
   volatile int abort;
   int mprefix[kFp8MaxGroups + 1];
   int offsets[kFp8MaxGroups + 1];
   float hmax[2][BM];
   alignas(16) float sb[2][2][128];      // per-row scales of B: [column half][parity][column]
-  alignas(16) uint8_t stage_out[EPI_WARPS][32 * ROW_STAGE];
 };
 
 // Byte offset of 16-byte piece v of staged row r: the pieces are permuted so that
@@ -84,7 +96,7 @@ __device__ __forceinline__ int stage_at(int r, int v) { return r * ROW_STAGE + (
 
 template <int AR>
 constexpr size_t smem_bytes() {
-  return Geo<AR>::STAGES * Geo<AR>::STAGE_BYTES + sizeof(Ctl) + 1024;
+  return Geo<AR>::STAGES * Geo<AR>::STAGE_BYTES + Geo<AR>::OUT_BYTES + sizeof(Ctl) + 1024;
 }
 
 // kind::f8f6f4: e4m3 A and B (format fields 0, both K-major), fp32 D.
@@ -242,7 +254,7 @@ __device__ __forceinline__ float silu_mul(float a, float b) { return __fdividef(
 template <int EPI, int AR, bool SB1>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
-                    const __grid_constant__ CUtensorMap tmB1, const Fp8Params p) {
+                    const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmOut, const Fp8Params p) {
   constexpr bool PAIR = EPI == FP8_SWIGLU || EPI == FP8_PAIR_F32;  // 128 columns of W1 and the same of W3
   constexpr bool F32 = EPI == FP8_F32 || EPI == FP8_PAIR_F32;
   constexpr bool ACT = EPI == FP8_SWIGLU || EPI == FP8_RELU;
@@ -251,13 +263,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   constexpr int STAGES = G::STAGES, STAGE_BYTES = G::STAGE_BYTES, A_ST = G::A_ST;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  Ctl* ctl = reinterpret_cast<Ctl*>(stages + STAGES * STAGE_BYTES);
+  uint8_t* out_stage = stages + STAGES * STAGE_BYTES;
+  Ctl* ctl = reinterpret_cast<Ctl*>(out_stage + G::OUT_BYTES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) { mbar_init(&ctl->full[s], 1); mbar_init(&ctl->empty[s], 1); }
     for (int a = 0; a < 2; ++a) { mbar_init(&ctl->tfull[a], 1); mbar_init(&ctl->tempty[a], EPI_WARPS); }
-    mbar_init(&ctl->drain, 1);
+    for (int a = 0; a < 2; ++a) mbar_init(&ctl->drain[a], 1);
     ctl->abort = 0;
     fence_mbarrier_init();
     tma_prefetch_desc(&tmA);
@@ -304,34 +317,38 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int s = 0; s < STAGES; ++s)
         if ((issued >> s) & 1u) mbar_wait(&ctl->full[s], (issued_phase >> s) & 1u, p.limit_ns);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
+  } else if (warp <= 2) {
+    // ------------------------------------------------------------ MMA issuers
     if (lane == 0) {
-      int stage = 0, acc = 0;
+      const int acc = warp - 1;  // this warp's accumulator: k-blocks acc, acc + 2, ... of the CTA's
+      int stage = 0, turn = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
+      const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * MMA_N);
       for (int64_t u = blockIdx.x; ok && item_at(ctl, p, u, w); u += gridDim.x) {
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (!mbar_wait_or_abort(&ctl->tempty[acc], acc_phase ^ 1u, &ctl->abort, p.err, p.limit_ns) ||
-              !mbar_wait_or_abort(&ctl->full[stage], phase, &ctl->abort, p.err, p.limit_ns)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(stages + stage * STAGE_BYTES);
-          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * MMA_N);
+          if (turn == acc) {
+            if (!mbar_wait_or_abort(&ctl->tempty[acc], acc_phase ^ 1u, &ctl->abort, p.err, p.limit_ns) ||
+                !mbar_wait_or_abort(&ctl->full[stage], phase, &ctl->abort, p.err, p.limit_ns)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = smem_u32(stages + stage * STAGE_BYTES);
 #pragma unroll
-          for (int k = 0; k < BK / 32; ++k)
-            umma_f8(d_tmem, sdesc_k_sw128(sa + k * 32), sdesc_k_sw128(sa + A_ST + k * 32), IDESC, k != 0 ? 1u : 0u);
-          umma_commit(&ctl->empty[stage]);
-          umma_commit(&ctl->tfull[acc]);
+            for (int k = 0; k < BK / 32; ++k)
+              umma_f8(d_tmem, sdesc_k_sw128(sa + k * 32), sdesc_k_sw128(sa + A_ST + k * 32), IDESC, k != 0 ? 1u : 0u);
+            umma_commit(&ctl->empty[stage]);
+            umma_commit(&ctl->tfull[acc]);
+            acc_phase ^= 1u;
+          }
+          turn ^= 1;
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-          if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
         }
       }
-      // Drain: all MMAs of this CTA complete before TMEM is freed.
-      umma_commit(&ctl->drain);
-      mbar_wait(&ctl->drain, 0, p.limit_ns);
+      // Drain: all MMAs of this thread complete before TMEM is freed.
+      umma_commit(&ctl->drain[acc]);
+      mbar_wait(&ctl->drain[acc], 0, p.limit_ns);
     }
   }
   } else {
@@ -339,7 +356,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     reg_inc<REGS_SUM>();
     const int q = warp & 3, half = (warp - 4) >> 2;
     const int r_in_tile = q * 32 + lane;
-    uint8_t* stg = ctl->stage_out[warp - 4];
+    uint8_t* stg = out_stage + (warp - 4) * (G::OUT_BYTES / EPI_WARPS);
+    constexpr bool TMA_OUT = AR == BM && EPI != FP8_PAIR_F32;
+    const bool storer = (threadIdx.x & 127) == 0;  // issues its warpgroup's TMA stores (ACT: the first one both's)
     // PAIR: columns [64 half, +64) of W1, then of W3; else columns [128 half, +128)
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t col0 = PAIR ? 64u * half : 128u * half, col2 = PAIR ? 128u + 64u * half : 128u * half + 64u;
@@ -416,9 +435,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (++acc_i == 2) { acc_i = 0; acc_phase ^= 1u; }
         if (!ok && !SB1) break;
       }
-      // Where warps meet at barriers, they leave an aborted CTA together.
-      if (SB1) ok = named_barrier_and(1 + half, 128, ok);
-      if (EPI == FP8_SWIGLU) ok = named_barrier_and(3, 256, ok);  // (the last tile's hmax has been read, too)
+      // Where warps meet at barriers, they leave an aborted CTA together.  (Also:
+      // the last tile's hmax has been read, and its stores have read out_stage.)
+      if (TMA_OUT && storer) bulk_wait_read();
+      if (EPI == FP8_SWIGLU || (EPI == FP8_RELU && TMA_OUT)) ok = named_barrier_and(3, 256, ok);
+      else if (TMA_OUT || SB1) ok = named_barrier_and(1 + half, 128, ok);
+      const bool by_tma = TMA_OUT && p.tma_out && ctl->offsets[w.g] + w.mt * BM + BM <= ctl->offsets[w.g + 1];
       if (ACT) {
         // activation, then codes with one scale for each 128 columns of a row
         constexpr int NV = PAIR ? 64 : 128;
@@ -435,18 +457,67 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           m = fmaxf(m, ctl->hmax[half ^ 1][r_in_tile]);
         }
         const Fp8Scale s = fp8_scale(m);
+        if (ok && vrow && n0 < p.N && (!PAIR || half == 0)) p.out_scales[static_cast<int64_t>(row) * bn_blocks + (n0 >> 7)] = s.scale;
         if (ok && vrow && n0 < p.N) {
           uint8_t* dst = static_cast<uint8_t*>(p.out) + static_cast<int64_t>(row) * p.ld_out + n0;
+          // PAIR: one box of 128 columns for both halves, else one for each
+          uint8_t* box = out_stage + (PAIR ? 0 : half * OUT_HALF) + r_in_tile * 128;
+          const int first = PAIR ? half * 4 : 0;
 #pragma unroll
           for (int i = 0; i < NV; i += 16) {
-            if (n0 + i < p.N)  // N is a multiple of 16
-              *reinterpret_cast<uint4*>(dst + i) = make_uint4(
-                  e4m3x4(acc[i] * s.inv, acc[i + 1] * s.inv, acc[i + 2] * s.inv, acc[i + 3] * s.inv),
-                  e4m3x4(acc[i + 4] * s.inv, acc[i + 5] * s.inv, acc[i + 6] * s.inv, acc[i + 7] * s.inv),
-                  e4m3x4(acc[i + 8] * s.inv, acc[i + 9] * s.inv, acc[i + 10] * s.inv, acc[i + 11] * s.inv),
-                  e4m3x4(acc[i + 12] * s.inv, acc[i + 13] * s.inv, acc[i + 14] * s.inv, acc[i + 15] * s.inv));
+            const uint4 v = make_uint4(
+                e4m3x4(acc[i] * s.inv, acc[i + 1] * s.inv, acc[i + 2] * s.inv, acc[i + 3] * s.inv),
+                e4m3x4(acc[i + 4] * s.inv, acc[i + 5] * s.inv, acc[i + 6] * s.inv, acc[i + 7] * s.inv),
+                e4m3x4(acc[i + 8] * s.inv, acc[i + 9] * s.inv, acc[i + 10] * s.inv, acc[i + 11] * s.inv),
+                e4m3x4(acc[i + 12] * s.inv, acc[i + 13] * s.inv, acc[i + 14] * s.inv, acc[i + 15] * s.inv));
+            if (by_tma) *reinterpret_cast<uint4*>(box + (((first + i / 16) ^ (r_in_tile & 7)) << 4)) = v;
+            else if (n0 + i < p.N) *reinterpret_cast<uint4*>(dst + i) = v;  // N is a multiple of 16
           }
-          if (!PAIR || half == 0) p.out_scales[static_cast<int64_t>(row) * bn_blocks + (n0 >> 7)] = s.scale;
+        }
+        if (by_tma && ok) {
+          fence_async_shared();
+          named_barrier(3, 256);
+          if (storer && (!PAIR || half == 0) && n0 < p.N) {
+            tma_store_3d(&tmOut, out_stage + (PAIR ? 0 : half * OUT_HALF), n0, ctl->offsets[w.g] + w.mt * BM, 0);
+            bulk_commit();
+          }
+        }
+      } else if (by_tma && ok) {
+        // a row's 128 bytes in each box, its 16-byte pieces permuted as the map's swizzle has them
+        constexpr int ELT = EPI == FP8_BF16 ? 2 : 4, BOX = 128 / ELT;
+        const float g = (F32 && p.row_gate != nullptr && vrow) ? p.row_gate[row] : 1.f;
+        const int n0 = w.nt * 256 + half * 128;
+        uint8_t* boxes = out_stage + half * OUT_HALF;
+#pragma unroll
+        for (int r = 0; r < 128 / BOX / 2; ++r) {  // two boxes at a time
+          if (r > 0) {
+            if (storer) bulk_wait_read();
+            named_barrier(1 + half, 128);
+          }
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+              const float* s = acc + (r * 2 + b) * BOX + v * (16 / ELT);
+              const uint4 q = EPI == FP8_BF16
+                                  ? make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]),
+                                               pack_bf16x2(s[4 % (16 / ELT)], s[5 % (16 / ELT)]),
+                                               pack_bf16x2(s[6 % (16 / ELT)], s[7 % (16 / ELT)]))
+                                  : make_uint4(__float_as_uint(s[0] * g), __float_as_uint(s[1] * g),
+                                               __float_as_uint(s[2] * g), __float_as_uint(s[3] * g));
+              *reinterpret_cast<uint4*>(boxes + b * 16384 + r_in_tile * 128 + ((v ^ (r_in_tile & 7)) << 4)) = q;
+            }
+          }
+          fence_async_shared();
+          named_barrier(1 + half, 128);
+          if (storer) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const int col = n0 + (r * 2 + b) * BOX;
+              if (col < p.N) tma_store_3d(&tmOut, boxes + b * 16384, col, ctl->offsets[w.g] + w.mt * BM, w.ks);
+            }
+            bulk_commit();
+          }
         }
       } else if (ok && warp_live) {
         // 64 bytes of every row at a time through shared memory, so that the
@@ -502,6 +573,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
     }
+    if (TMA_OUT && storer) bulk_wait();
   }
 
   tc_fence_before();
@@ -624,7 +696,7 @@ bool map_3d(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint64_
   const uint64_t dims[3] = {K, rows, mats};
   const uint64_t strides[2] = {ld, gs};
   const uint32_t box[3] = {static_cast<uint32_t>(BK), box_rows, 1};
-  return make_map_u8(m, base, 3, dims, strides, box);
+  return make_map_nd(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, 3, dims, strides, box);
 }
 
 template <int EPI, int AR, bool SB1>
@@ -634,7 +706,7 @@ cudaError_t launch_t(const Fp8Plan& pl, int num_sms, cudaStream_t s) {
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(&fp8_gemm_kernel<EPI, AR, SB1>),
                                       static_cast<int>(bytes));
   if (e != cudaSuccess) return e;
-  return launch_pdl(fp8_gemm_kernel<EPI, AR, SB1>, dim3(num_sms), dim3(NUM_THREADS), bytes, s, pl.a, pl.b0, pl.b1, pl.p);
+  return launch_pdl(fp8_gemm_kernel<EPI, AR, SB1>, dim3(num_sms), dim3(NUM_THREADS), bytes, s, pl.a, pl.b0, pl.b1, pl.out, pl.p);
 }
 
 template <int EPI>
@@ -686,7 +758,7 @@ cudaError_t plan_fp8(const Fp8Args& g, Fp8Plan* pl, const char** why) {
   const uint64_t as[1] = {static_cast<uint64_t>(g.lda)};
   const uint32_t abox[2] = {static_cast<uint32_t>(BK), static_cast<uint32_t>(pl->ar)};
   const uint64_t K = g.K, N = g.N, G = g.G, ldb = g.ldb, gsb = g.gsb;
-  if (!make_map_u8(&pl->a, g.A, 2, ad, as, abox) || !map_3d(&pl->b0, g.B0, K, N, G, ldb, gsb, pair ? 128 : 256) ||
+  if (!make_map_nd(&pl->a, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.A, 2, ad, as, abox) || !map_3d(&pl->b0, g.B0, K, N, G, ldb, gsb, pair ? 128 : 256) ||
       !map_3d(&pl->b1, pair ? g.B1 : g.B0, K, N, G, ldb, gsb, 128)) {
     *why = "cuTensorMapEncodeTiled failed (alignment or driver entry point)";
     return cudaErrorInvalidValue;
@@ -715,6 +787,22 @@ cudaError_t plan_fp8(const Fp8Args& g, Fp8Plan* pl, const char** why) {
   p.vec_out = ((reinterpret_cast<uintptr_t>(g.out) | static_cast<uintptr_t>(g.ld_out * elt) |
                 static_cast<uintptr_t>(static_cast<int64_t>(g.N) * elt) | static_cast<uintptr_t>(g.split_stride * elt) |
                 static_cast<uintptr_t>(g.pair_stride * elt)) & 15) == 0;
+  // whole tiles of the output by TMA, where its rows allow it
+  const bool act = g.epi == FP8_SWIGLU || g.epi == FP8_RELU;
+  const int oelt = act ? 1 : elt;
+  p.tma_out = 0;
+  pl->out = pl->a;
+  if (pl->ar == 128 && g.epi != FP8_PAIR_F32 &&
+      ((reinterpret_cast<uintptr_t>(g.out) | static_cast<uintptr_t>(g.ld_out * oelt) |
+        static_cast<uintptr_t>(g.split_stride * oelt)) & 15) == 0) {
+    const CUtensorMapDataType type = act ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                         : elt == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    const uint64_t od[3] = {N, static_cast<uint64_t>(g.a_rows), static_cast<uint64_t>(p.ksplit)};
+    const uint64_t os[2] = {static_cast<uint64_t>(g.ld_out) * oelt,
+                            static_cast<uint64_t>(p.ksplit > 1 ? g.split_stride : g.a_rows * g.ld_out) * oelt};
+    const uint32_t obox[3] = {static_cast<uint32_t>(128 / oelt), 128, 1};
+    p.tma_out = make_map_nd(&pl->out, type, g.out, 3, od, os, obox);
+  }
   p.row_gate = g.row_gate;
   p.offsets = g.offsets;
   p.err = g.err;

@@ -550,15 +550,15 @@ bool make_map_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, uin
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_map_u8(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
-                 const uint32_t* box) {
+bool make_map_nd(CUtensorMap* m, CUtensorMapDataType type, const void* base, int rank, const uint64_t* dims,
+                 const uint64_t* strides, const uint32_t* box) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr || rank < 2 || rank > 3) return false;
   cuuint64_t d[3], st[2];
   cuuint32_t b[3], estr[3] = {1, 1, 1};
   for (int i = 0; i < rank; ++i) { d[i] = dims[i]; b[i] = box[i]; }
   for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, b, estr,
+  return enc(m, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, b, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

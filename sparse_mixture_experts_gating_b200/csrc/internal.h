@@ -180,10 +180,10 @@ cudaError_t launch_gemm_tc(const TcGemmPlan& plan, int num_sms, cudaStream_t s);
 bool make_map_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t rows, uint64_t cols,
                  uint32_t elem_bytes, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle);
 
-// Tensor of bytes of rank 2 or 3 (dims innermost first, strides in bytes from
-// the second dimension on) -> map with the given box and 128-byte swizzle.
-bool make_map_u8(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
-                 const uint32_t* box);
+// Tensor of rank 2 or 3 (dims innermost first, strides in bytes from the
+// second dimension on) -> map with the given box and 128-byte swizzle.
+bool make_map_nd(CUtensorMap* m, CUtensorMapDataType type, const void* base, int rank, const uint64_t* dims,
+                 const uint64_t* strides, const uint32_t* box);
 
 // ---------------------------------------------------------------- 4-bit weights
 // Codes in tiles of 128 rows x 64 elements, each tile 4 KB contiguous (row r
