@@ -53,6 +53,7 @@ constexpr int NUM_THREADS = 384;
 constexpr int REGS_START = 168, REGS_FEED = 40, REGS_SUM = 232;
 static_assert(REGS_FEED + 2 * REGS_SUM <= 3 * REGS_START, "the registers of the launch");
 constexpr int EPI_WARPS = 8;
+constexpr int SB_SLOTS = 4;              // k-blocks of column scales in flight (SB1)
 constexpr uint32_t TMEM_COLS = 2 * MMA_N;
 constexpr int ROW_STAGE = 64;           // bytes per staged output row of a warp's own stores
 constexpr int OUT_HALF = 2 * 16384;     // two boxes of 128 rows x 128 bytes of a warpgroup's TMA stores
@@ -87,7 +88,10 @@ struct Ctl {
   int mprefix[kFp8MaxGroups + 1];
   int offsets[kFp8MaxGroups + 1];
   float hmax[2][BM];
-  alignas(16) float sb[2][2][128];      // per-row scales of B: [column half][parity][column]
+  // per-row scales of B (SB1): a ring of k-blocks' 256 columns
+  uint64_t sfull[SB_SLOTS];
+  uint64_t sempty[SB_SLOTS];
+  alignas(16) float sb[SB_SLOTS][MMA_N];
 };
 
 // Byte offset of 16-byte piece v of staged row r: the pieces are permuted so that
@@ -211,6 +215,15 @@ __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// One fp32 number, copied without waiting.
+__device__ __forceinline__ void cp_async4(float* dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// Arrive on `bar` (within its count) when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // Waits for the warp's TMEM loads; t passes through, so that no use of it moves up.
 __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&t)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -249,7 +262,14 @@ __device__ __forceinline__ void promote32(float* acc, const uint32_t (&t)[32], f
   }
 }
 
-__device__ __forceinline__ float silu_mul(float a, float b) { return __fdividef(a, 1.f + __expf(-a)) * b; }
+// silu(a) * b from the special function unit's exponential and reciprocal (each
+// good to two units; 0 once e^-a overflows, the limit of silu).
+__device__ __forceinline__ float silu_mul(float a, float b) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return a * b * r;
+}
 
 template <int EPI, int AR, bool SB1>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
@@ -271,6 +291,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int s = 0; s < STAGES; ++s) { mbar_init(&ctl->full[s], 1); mbar_init(&ctl->empty[s], 1); }
     for (int a = 0; a < 2; ++a) { mbar_init(&ctl->tfull[a], 1); mbar_init(&ctl->tempty[a], EPI_WARPS); }
     for (int a = 0; a < 2; ++a) mbar_init(&ctl->drain[a], 1);
+    for (int s = 0; s < SB_SLOTS; ++s) { mbar_init(&ctl->sfull[s], 32); mbar_init(&ctl->sempty[s], EPI_WARPS); }
     ctl->abort = 0;
     fence_mbarrier_init();
     tma_prefetch_desc(&tmA);
@@ -350,6 +371,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       umma_commit(&ctl->drain[acc]);
       mbar_wait(&ctl->drain[acc], 0, p.limit_ns);
     }
+  } else if (SB1) {
+    // ------------------------------------------------------------ column scales
+    // (fetched by the summing threads themselves, a column each, one k-block's
+    // scales took two microseconds: a row of 65 scales shares no line with the next)
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; ok && item_at(ctl, p, u, w); u += gridDim.x) {
+      const int col = w.nt * 256 + lane;
+      const float* sb = p.sb0 + w.g * p.sb_gs + static_cast<int64_t>(col) * p.num_kb;
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_or_abort(&ctl->sempty[slot], phase ^ 1u, &ctl->abort, p.err, p.limit_ns));
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < MMA_N / 32; ++i)
+          if (col + 32 * i < p.N)
+            cp_async4(&ctl->sb[slot][lane + 32 * i], sb + static_cast<int64_t>(32 * i) * p.num_kb + kb);
+        cp_async_arrive(&ctl->sfull[slot]);
+        if (++slot == SB_SLOTS) { slot = 0; phase ^= 1u; }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
   } else {
     // ------------------------------------------------------------ promotion and epilogue
@@ -362,8 +406,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // PAIR: columns [64 half, +64) of W1, then of W3; else columns [128 half, +128)
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t col0 = PAIR ? 64u * half : 128u * half, col2 = PAIR ? 128u + 64u * half : 128u * half + 64u;
-    int acc_i = 0;
-    uint32_t acc_phase = 0;
+    int acc_i = 0, slot = 0;
+    uint32_t acc_phase = 0, slot_phase = 0;
     bool ok = true;
     for (int64_t u = blockIdx.x; ok && item_at(ctl, p, u, w); u += gridDim.x) {
       const int m_local = w.mt * BM + r_in_tile;
@@ -376,7 +420,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const float* sa = p.sa + (vrow ? static_cast<int64_t>(row) : 0) * p.sa_ld;
       const float* sb0 = p.sb0 + w.g * p.sb_gs + (SB1 ? 0 : static_cast<int64_t>(nb) * p.num_kb);
       const float* sb1 = PAIR ? p.sb1 + w.g * p.sb_gs + static_cast<int64_t>(nb) * p.num_kb : nullptr;
-      const int my_n = w.nt * 256 + half * 128 + (threadIdx.x - 128 - half * 128);  // SB1: the column this thread fetches
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
@@ -384,11 +427,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       auto scale_a = [&](int kb) { return vrow && kb < w.kb1 ? __ldg(sa + kb) : 0.f; };
       auto scale_b0 = [&](int kb) { return !SB1 && kb < w.kb1 ? __ldg(sb0 + kb) : 1.f; };
       auto scale_b1 = [&](int kb) { return PAIR && kb < w.kb1 ? __ldg(sb1 + kb) : 1.f; };
-      auto scale_bc = [&](int kb) {
-        return SB1 && kb < w.kb1 && my_n < p.N ? __ldg(sb0 + static_cast<int64_t>(my_n) * p.num_kb + kb) : 0.f;
-      };
       float a0 = scale_a(w.kb0), a1 = scale_a(w.kb0 + 1), b0 = scale_b0(w.kb0), b1 = scale_b0(w.kb0 + 1);
-      float c0 = scale_b1(w.kb0), c1 = scale_b1(w.kb0 + 1), n0_ = scale_bc(w.kb0), n1_ = scale_bc(w.kb0 + 1);
+      float c0 = scale_b1(w.kb0), c1 = scale_b1(w.kb0 + 1);
 #pragma unroll 1
       for (int kb = w.kb0; kb < w.kb1; ++kb) {
         const float s0 = a0 * b0, s1 = PAIR ? a0 * c0 : s0;
@@ -396,13 +436,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         a1 = scale_a(kb + 2);
         b1 = scale_b0(kb + 2);
         c1 = scale_b1(kb + 2);
-        float* sbs = ctl->sb[half][acc_i];  // (turns with the accumulator: the last block's may still be read)
-        if (SB1) {  // this half's 128 scales of B, one per thread
-          sbs[threadIdx.x - 128 - half * 128] = n0_;
-          n0_ = n1_;
-          n1_ = scale_bc(kb + 2);
-          named_barrier(1 + half, 128);
-        }
+        const float* sbs = ctl->sb[slot] + half * 128;
+        if (SB1)
+          ok = ok && __all_sync(0xffffffffu,
+                                mbar_wait_or_abort(&ctl->sfull[slot], slot_phase, &ctl->abort, p.err, p.limit_ns));
         ok = ok && __all_sync(0xffffffffu,
                               mbar_wait_or_abort(&ctl->tfull[acc_i], acc_phase, &ctl->abort, p.err, p.limit_ns));
         if (ok) {
@@ -432,14 +469,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (lane == 0) mbar_arrive(&ctl->tempty[acc_i]);
           }
         }
+        if (SB1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->sempty[slot]);
+          if (++slot == SB_SLOTS) { slot = 0; slot_phase ^= 1u; }
+        }
         if (++acc_i == 2) { acc_i = 0; acc_phase ^= 1u; }
-        if (!ok && !SB1) break;
+        if (!ok) break;
       }
       // Where warps meet at barriers, they leave an aborted CTA together.  (Also:
       // the last tile's hmax has been read, and its stores have read out_stage.)
       if (TMA_OUT && storer) bulk_wait_read();
       if (EPI == FP8_SWIGLU || (EPI == FP8_RELU && TMA_OUT)) ok = named_barrier_and(3, 256, ok);
-      else if (TMA_OUT || SB1) ok = named_barrier_and(1 + half, 128, ok);
+      else if (TMA_OUT) ok = named_barrier_and(1 + half, 128, ok);
       const bool by_tma = TMA_OUT && p.tma_out && ctl->offsets[w.g] + w.mt * BM + BM <= ctl->offsets[w.g + 1];
       if (ACT) {
         // activation, then codes with one scale for each 128 columns of a row
@@ -449,7 +491,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           acc[i] = PAIR ? silu_mul(acc[i], acc[(i + 64) & 127]) : fmaxf(acc[i], 0.f);
-          m = fmaxf(m, n0 + i < p.N ? fabsf(acc[i]) : 0.f);
+          m = fmaxf(m, fabsf(acc[i]));
+        }
+        if (n0 + NV > p.N) {  // columns past N are not the row's
+          m = 0.f;
+#pragma unroll
+          for (int i = 0; i < NV; ++i) m = fmaxf(m, n0 + i < p.N ? fabsf(acc[i]) : 0.f);
         }
         if (PAIR) {  // the row's other 64 columns are with the other half's thread
           ctl->hmax[half][r_in_tile] = m;
