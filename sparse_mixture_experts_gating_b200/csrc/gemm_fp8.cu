@@ -271,6 +271,11 @@ __device__ __forceinline__ float silu_mul(float a, float b) {
   return a * b * r;
 }
 
+template <int BYTES>
+struct OutWord { using type = uint16_t; };
+template <>
+struct OutWord<4> { using type = uint32_t; };
+
 template <int EPI, int AR, bool SB1>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
@@ -567,33 +572,31 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
       } else if (ok && warp_live) {
-        // 64 bytes of every row at a time through shared memory, so that the
-        // stores run along rows
-        constexpr int ELT = EPI == FP8_BF16 ? 2 : 4, PER = 64 / ELT;
+        // through shared memory, so that the stores run along rows: 64 bytes of
+        // every row at a time, or where the rows' alignment wants one element a
+        // store, as many as there is room for
+        constexpr int ELT = EPI == FP8_BF16 ? 2 : 4;
         const float g = (F32 && p.row_gate != nullptr && vrow) ? p.row_gate[row] : 1.f;
         const int n0 = PAIR ? w.nt * 128 + half * 64 : w.nt * 256 + half * 128;
-        const int nrows = min(32, ctl->offsets[w.g + 1] - (ctl->offsets[w.g] + w.mt * BM + q * 32));
         const int64_t row_base = ctl->offsets[w.g] + w.mt * BM + q * 32;
+        const int nrows = min(32, ctl->offsets[w.g + 1] - static_cast<int>(row_base));
         uint8_t* out = static_cast<uint8_t*>(p.out) + static_cast<int64_t>(w.ks) * p.split_stride * ELT;
+        auto piece = [&](int first) {  // 16 bytes of this lane's row, from column `first` of its 128 on
+          const float* s = acc + first;
+          if (ELT == 2)
+            return make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
+          return make_uint4(__float_as_uint(s[0] * g), __float_as_uint(s[1] * g), __float_as_uint(s[2] * g),
+                            __float_as_uint(s[3] * g));
+        };
+        if (p.vec_out) {
+          constexpr int PER = 64 / ELT;
 #pragma unroll
-        for (int c = 0; c < 128 / PER; ++c) {
+          for (int c = 0; c < 128 / PER; ++c) {
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            uint4& piece = *reinterpret_cast<uint4*>(stg + stage_at(lane, v));
-            if (EPI == FP8_BF16) {
-              const float* s = acc + c * PER + v * 8;
-              piece = make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]),
-                                   pack_bf16x2(s[6], s[7]));
-            } else {
-              const float* s = acc + c * PER + v * 4;
-              piece = make_uint4(__float_as_uint(s[0] * g), __float_as_uint(s[1] * g), __float_as_uint(s[2] * g),
-                                   __float_as_uint(s[3] * g));
-            }
-          }
-          __syncwarp();
-          const int col = n0 + (PAIR ? c % 4 : c) * PER;
-          if (PAIR && c == 4) out += p.pair_stride * ELT;  // W3's columns
-          if (p.vec_out) {
+            for (int v = 0; v < 4; ++v) *reinterpret_cast<uint4*>(stg + stage_at(lane, v)) = piece(c * PER + v * (16 / ELT));
+            __syncwarp();
+            const int col = n0 + (PAIR ? c % (64 / PER) : c) * PER;
+            if (PAIR && c == 64 / PER) out += p.pair_stride * ELT;  // W3's columns
             const int seg = lane & 3;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -602,21 +605,31 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 *reinterpret_cast<uint4*>(out + ((row_base + rr) * p.ld_out + col) * ELT + seg * 16) =
                     *reinterpret_cast<const uint4*>(stg + stage_at(rr, seg));
             }
-          } else {
-#pragma unroll 1
-            for (int i = lane; i < 32 * PER; i += 32) {
-              const int rr = i / PER, cc = i % PER, at = stage_at(rr, cc * ELT >> 4) + (cc * ELT & 15);
-              if (rr < nrows && col + cc < p.N) {
-                if (EPI == FP8_BF16)
-                  *reinterpret_cast<uint16_t*>(out + ((row_base + rr) * p.ld_out + col + cc) * ELT) =
-                      *reinterpret_cast<const uint16_t*>(stg + at);
-                else
-                  *reinterpret_cast<float*>(out + ((row_base + rr) * p.ld_out + col + cc) * ELT) =
-                      *reinterpret_cast<const float*>(stg + at);
+            __syncwarp();
+          }
+        } else if (!PAIR) {  // (a cut first projection has N a multiple of 16)
+          constexpr int WIDE = G::OUT_BYTES / EPI_WARPS / 32;  // bytes of a row laid out at once
+          constexpr int PER = WIDE / ELT, PIECES = WIDE / 16, SWAP = PIECES < 8 ? PIECES - 1 : 7;
+          using Word = typename OutWord<ELT>::type;
+#pragma unroll
+          for (int c = 0; c < 128 / PER; ++c) {
+#pragma unroll
+            for (int v = 0; v < PIECES; ++v)
+              *reinterpret_cast<uint4*>(stg + lane * WIDE + ((v ^ (lane & SWAP)) << 4)) = piece(c * PER + v * (16 / ELT));
+            __syncwarp();
+            const int col = n0 + c * PER;
+#pragma unroll 4
+            for (int rr = 0; rr < nrows; ++rr) {
+              Word* dst = reinterpret_cast<Word*>(out) + (row_base + rr) * p.ld_out + col;
+#pragma unroll
+              for (int e0 = 0; e0 < PER; e0 += 32) {
+                const int e = e0 + lane;
+                if (e < PER && col + e < p.N)
+                  dst[e] = *reinterpret_cast<const Word*>(stg + rr * WIDE + (((e * ELT >> 4) ^ (rr & SWAP)) << 4) + (e * ELT & 15));
               }
             }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
     }
@@ -777,7 +790,7 @@ int fp8_ksplit(int64_t rows, int G, int N, int K) {
   // SMs) ranges of `per` k-blocks, each followed by an epilogue (5 k-blocks for
   // a full tile; next to nothing for a few rows, whose weight stream goes on
   // under it); every partial is written and read once more (a k-block's time
-  // moves 1.6 MB), and a cut product needs a second launch (8 k-blocks of the
+  // moves 2.7 MB), and a cut product needs a second launch (8 k-blocks of the
   // tensor cores' time, 3.5 of the weight stream's).  Rows count in powers of
   // two, so that the choice is constant between them.
   int64_t r2 = 1;
@@ -789,7 +802,7 @@ int fp8_ksplit(int64_t rows, int G, int N, int K) {
     const int64_t per = (num_kb + ks - 1) / ks;
     const int64_t ranges = (num_kb + per - 1) / per;
     const int64_t t = (tiles * ranges + kSplitTargetCtas - 1) / kSplitTargetCtas * (10 * per + epi) +
-                      r2 * N * ranges / 20000 + launch;
+                      r2 * N * ranges / 34000 + launch;
     if (t * 32 < best_t * 31) { best = ranges; best_t = t; }
   }
   return static_cast<int>(best);
