@@ -34,7 +34,10 @@ cudaError_t launch_quantize_fp8(const QuantFp8Args& a, cudaStream_t s);
 // with a scale for each 128 columns of a row.
 // FP8_PAIR_F32: the two products of a SwiGLU layer as they are, W3's
 // pair_stride elements behind W1's (one partial per K range).
-enum Fp8Epi { FP8_BF16 = 0, FP8_F32 = 1, FP8_SWIGLU = 2, FP8_RELU = 3, FP8_PAIR_F32 = 4 };
+// FP8_GATE_H16: row_gate times the product in fp16, each 128 columns of a row
+// by a power of two that takes their largest to [2^14, 2^15); out_scales holds
+// its inverse.  (Groups of over 64 rows at most, so of whole tiles.)
+enum Fp8Epi { FP8_BF16 = 0, FP8_F32 = 1, FP8_SWIGLU = 2, FP8_RELU = 3, FP8_PAIR_F32 = 4, FP8_GATE_H16 = 5 };
 
 struct Fp8Args {
   int epi;
@@ -53,7 +56,7 @@ struct Fp8Args {
   int b_rows;              // rows of B under one scale: 128 or 1
   void* out;               // bf16 / fp32 [a_rows][N], rows ld_out elements apart; codes for the activations
   int64_t ld_out;
-  float* out_scales;       // activations: [a_rows][ceil(N / 128)]
+  float* out_scales;       // activations, FP8_GATE_H16: [a_rows][ceil(N / 128)]
   int ksplit;
   int64_t split_stride;    // elements between the partials of consecutive K ranges
   int64_t pair_stride;     // FP8_PAIR_F32
@@ -120,5 +123,20 @@ struct Fp8HiddenArgs {
   float* Hs;    // [rows][ceil(N / 128)]
 };
 cudaError_t launch_fp8_hidden(const Fp8HiddenArgs& a, int num_sms, cudaStream_t s);
+
+// y_t = sum over token t's kept choices j (in order) of their rows of Y (fp16,
+// times the scale of each 128 columns), then of the shared experts' rows
+// *shared_base + s * T + t.  d a multiple of 8.
+struct Fp8CombineArgs {
+  int64_t T;
+  int k, d, n_shared;
+  const int32_t* dest_row;     // [T][k], -1: dropped
+  const int32_t* shared_base;
+  const uint16_t* Y;           // [rows][d]
+  const float* scales;         // [rows][ceil(d / 128)]
+  void* y;                     // [T][d] bf16
+  float* y_f32;                // [T][d] or NULL
+};
+cudaError_t launch_fp8_combine(const Fp8CombineArgs& a, cudaStream_t s);
 
 }  // namespace moe

@@ -271,6 +271,25 @@ __device__ __forceinline__ float silu_mul(float a, float b) {
   return a * b * r;
 }
 
+// 16 bytes of an output row: eight bf16, eight fp16 scaled by g, or four fp32 times g.
+template <int EPI>
+__device__ __forceinline__ uint4 out_piece(const float* s, float g) {
+  if constexpr (EPI == FP8_BF16) {
+    return make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
+  } else if constexpr (EPI == FP8_GATE_H16) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(s[2 * i] * g, s[2 * i + 1] * g);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    return make_uint4(__float_as_uint(s[0] * g), __float_as_uint(s[1] * g), __float_as_uint(s[2] * g),
+                      __float_as_uint(s[3] * g));
+  }
+}
+
 template <int BYTES>
 struct OutWord { using type = uint16_t; };
 template <>
@@ -487,6 +506,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (TMA_OUT && storer) bulk_wait_read();
       if (EPI == FP8_SWIGLU || (EPI == FP8_RELU && TMA_OUT)) ok = named_barrier_and(3, 256, ok);
       else if (TMA_OUT) ok = named_barrier_and(1 + half, 128, ok);
+      // FP8_GATE_H16: this row's 128 columns by one power of two
+      float h16_scale = 1.f;
+      if (EPI == FP8_GATE_H16) {
+        float m = 0.f;
+        const int n0 = w.nt * 256 + half * 128;
+        if (n0 + 128 <= p.N) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) m = fmaxf(m, fabsf(acc[i]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) m = fmaxf(m, n0 + i < p.N ? fabsf(acc[i]) : 0.f);
+        }
+        const float g = vrow ? p.row_gate[row] : 0.f;
+        const int ex = static_cast<int>(__float_as_uint(fabsf(m * g)) >> 23);  // 2^(ex - 127) <= m g < 2^(ex - 126)
+        const int inv = max(ex - 14, 1);
+        h16_scale = g * __uint_as_float(static_cast<uint32_t>(254 - inv) << 23);
+        if (vrow && n0 < p.N)
+          p.out_scales[static_cast<int64_t>(row) * ((p.N + 127) >> 7) + (n0 >> 7)] = __uint_as_float(static_cast<uint32_t>(inv) << 23);
+      }
       const bool by_tma = TMA_OUT && p.tma_out && ctl->offsets[w.g] + w.mt * BM + BM <= ctl->offsets[w.g + 1];
       if (ACT) {
         // activation, then codes with one scale for each 128 columns of a row
@@ -536,7 +574,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       } else if (by_tma && ok) {
         // a row's 128 bytes in each box, its 16-byte pieces permuted as the map's swizzle has them
-        constexpr int ELT = EPI == FP8_BF16 ? 2 : 4, BOX = 128 / ELT;
+        constexpr int ELT = EPI == FP8_BF16 || EPI == FP8_GATE_H16 ? 2 : 4, BOX = 128 / ELT;
         const float g = (F32 && p.row_gate != nullptr && vrow) ? p.row_gate[row] : 1.f;
         const int n0 = w.nt * 256 + half * 128;
         uint8_t* boxes = out_stage + half * OUT_HALF;
@@ -551,12 +589,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
             for (int v = 0; v < 8; ++v) {
               const float* s = acc + (r * 2 + b) * BOX + v * (16 / ELT);
-              const uint4 q = EPI == FP8_BF16
-                                  ? make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]),
-                                               pack_bf16x2(s[4 % (16 / ELT)], s[5 % (16 / ELT)]),
-                                               pack_bf16x2(s[6 % (16 / ELT)], s[7 % (16 / ELT)]))
-                                  : make_uint4(__float_as_uint(s[0] * g), __float_as_uint(s[1] * g),
-                                               __float_as_uint(s[2] * g), __float_as_uint(s[3] * g));
+              const uint4 q = out_piece<EPI>(s, EPI == FP8_GATE_H16 ? h16_scale : g);
               *reinterpret_cast<uint4*>(boxes + b * 16384 + r_in_tile * 128 + ((v ^ (r_in_tile & 7)) << 4)) = q;
             }
           }
@@ -575,19 +608,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // through shared memory, so that the stores run along rows: 64 bytes of
         // every row at a time, or where the rows' alignment wants one element a
         // store, as many as there is room for
-        constexpr int ELT = EPI == FP8_BF16 ? 2 : 4;
+        constexpr int ELT = EPI == FP8_BF16 || EPI == FP8_GATE_H16 ? 2 : 4;
         const float g = (F32 && p.row_gate != nullptr && vrow) ? p.row_gate[row] : 1.f;
         const int n0 = PAIR ? w.nt * 128 + half * 64 : w.nt * 256 + half * 128;
         const int64_t row_base = ctl->offsets[w.g] + w.mt * BM + q * 32;
         const int nrows = min(32, ctl->offsets[w.g + 1] - static_cast<int>(row_base));
         uint8_t* out = static_cast<uint8_t*>(p.out) + static_cast<int64_t>(w.ks) * p.split_stride * ELT;
-        auto piece = [&](int first) {  // 16 bytes of this lane's row, from column `first` of its 128 on
-          const float* s = acc + first;
-          if (ELT == 2)
-            return make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
-          return make_uint4(__float_as_uint(s[0] * g), __float_as_uint(s[1] * g), __float_as_uint(s[2] * g),
-                            __float_as_uint(s[3] * g));
-        };
+        auto piece = [&](int first) { return out_piece<EPI>(acc + first, EPI == FP8_GATE_H16 ? h16_scale : g); };
         if (p.vec_out) {
           constexpr int PER = 64 / ELT;
 #pragma unroll
@@ -750,6 +777,53 @@ __global__ void __launch_bounds__(256) fp8_hidden_kernel(const Fp8HiddenArgs a) 
   }
 }
 
+// ---------------------------------------------------------------- combine
+// Thread: eight columns of a token, all of its rows' 16 bytes in flight.
+template <int K>
+__global__ void __launch_bounds__(256) fp8_combine_kernel(const Fp8CombineArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t vpr = static_cast<uint32_t>(a.d) >> 3;
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;  // T * d < 2^32
+  const uint32_t t = i / vpr, v = i - t * vpr;
+  if (t >= static_cast<uint64_t>(a.T)) return;
+  const int nb = (a.d + 127) >> 7, b = static_cast<int>(v >> 4);
+  const uint4* Y = reinterpret_cast<const uint4*>(a.Y);
+  uint4 q[K];
+  float s[K];
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    const int64_t row = a.dest_row[static_cast<int64_t>(t) * K + j];
+    q[j] = row >= 0 ? __ldcs(Y + row * vpr + v) : make_uint4(0u, 0u, 0u, 0u);
+    s[j] = row >= 0 ? a.scales[row * nb + b] : 0.f;
+  }
+  float acc[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) acc[c] = 0.f;
+  auto add = [&](const uint4& u, float f) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[c]));
+      acc[2 * c] = fmaf(h.x, f, acc[2 * c]);
+      acc[2 * c + 1] = fmaf(h.y, f, acc[2 * c + 1]);
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < K; ++j) add(q[j], s[j]);
+  for (int e = 0; e < a.n_shared; ++e) {  // shared experts after the routed sum
+    const int64_t row = *a.shared_base + e * a.T + t;
+    add(Y[row * vpr + v], a.scales[row * nb + b]);
+  }
+  const int64_t at = static_cast<int64_t>(t) * vpr + v;
+  if (a.y_f32 != nullptr) {
+    reinterpret_cast<float4*>(a.y_f32)[2 * at] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    reinterpret_cast<float4*>(a.y_f32)[2 * at + 1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+  }
+  reinterpret_cast<uint4*>(a.y)[at] = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
+                                                  pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
+}
+
 // ---------------------------------------------------------------- host
 bool map_3d(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint64_t mats, uint64_t ld, uint64_t gs,
             uint32_t box_rows) {
@@ -811,6 +885,10 @@ int fp8_ksplit(int64_t rows, int G, int N, int K) {
 cudaError_t plan_fp8(const Fp8Args& g, Fp8Plan* pl, const char** why) {
   *why = nullptr;
   const bool pair = g.epi == FP8_SWIGLU || g.epi == FP8_PAIR_F32;
+  if (g.epi == FP8_GATE_H16 && (g.max_group_rows <= 64 || g.b_rows == 1 || g.row_gate == nullptr)) {
+    *why = "8-bit product: the fp16 epilogue takes whole tiles and a gate";
+    return cudaErrorInvalidValue;
+  }
   pl->epi = g.epi;
   pl->sb1 = g.b_rows == 1;
   pl->ar = pl->sb1 ? 128 : g.max_group_rows <= 32 ? 32 : g.max_group_rows <= 64 ? 64 : 128;
@@ -843,7 +921,7 @@ cudaError_t plan_fp8(const Fp8Args& g, Fp8Plan* pl, const char** why) {
   p.split_stride = g.split_stride;
   p.pair_stride = g.pair_stride;
   p.out_scales = g.out_scales;
-  const int elt = g.epi == FP8_BF16 ? 2 : 4;
+  const int elt = g.epi == FP8_BF16 || g.epi == FP8_GATE_H16 ? 2 : 4;
   p.vec_out = ((reinterpret_cast<uintptr_t>(g.out) | static_cast<uintptr_t>(g.ld_out * elt) |
                 static_cast<uintptr_t>(static_cast<int64_t>(g.N) * elt) | static_cast<uintptr_t>(g.split_stride * elt) |
                 static_cast<uintptr_t>(g.pair_stride * elt)) & 15) == 0;
@@ -856,6 +934,7 @@ cudaError_t plan_fp8(const Fp8Args& g, Fp8Plan* pl, const char** why) {
       ((reinterpret_cast<uintptr_t>(g.out) | static_cast<uintptr_t>(g.ld_out * oelt) |
         static_cast<uintptr_t>(g.split_stride * oelt)) & 15) == 0) {
     const CUtensorMapDataType type = act ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                         : g.epi == FP8_GATE_H16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                          : elt == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
     const uint64_t od[3] = {N, static_cast<uint64_t>(g.a_rows), static_cast<uint64_t>(p.ksplit)};
     const uint64_t os[2] = {static_cast<uint64_t>(g.ld_out) * oelt,
@@ -874,6 +953,7 @@ cudaError_t launch_fp8(const Fp8Plan& pl, int num_sms, cudaStream_t s) {
   switch (pl.epi) {
     case FP8_BF16: return launch_ar<FP8_BF16>(pl, num_sms, s);
     case FP8_F32: return launch_ar<FP8_F32>(pl, num_sms, s);
+    case FP8_GATE_H16: return launch_t<FP8_GATE_H16, 128, false>(pl, num_sms, s);
     case FP8_PAIR_F32: return launch_ar<FP8_PAIR_F32>(pl, num_sms, s);
     case FP8_SWIGLU: return launch_ar<FP8_SWIGLU>(pl, num_sms, s);
     default: return launch_ar<FP8_RELU>(pl, num_sms, s);
@@ -897,6 +977,22 @@ cudaError_t launch_fp8_hidden(const Fp8HiddenArgs& a, int num_sms, cudaStream_t 
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>((items + 15) / 16, num_sms * 8)));
   return a.pair_stride > 0 ? launch_pdl(fp8_hidden_kernel<true>, grid, dim3(256), 0, s, a)
                            : launch_pdl(fp8_hidden_kernel<false>, grid, dim3(256), 0, s, a);
+}
+
+cudaError_t launch_fp8_combine(const Fp8CombineArgs& a, cudaStream_t s) {
+  const uint64_t n = static_cast<uint64_t>(a.T) * (a.d / 8);  // below 2^29
+  if (n == 0) return cudaSuccess;
+  const dim3 grid(static_cast<unsigned>((n + 255) / 256));
+  switch (a.k) {
+    case 1: return launch_pdl(fp8_combine_kernel<1>, grid, dim3(256), 0, s, a);
+    case 2: return launch_pdl(fp8_combine_kernel<2>, grid, dim3(256), 0, s, a);
+    case 3: return launch_pdl(fp8_combine_kernel<3>, grid, dim3(256), 0, s, a);
+    case 4: return launch_pdl(fp8_combine_kernel<4>, grid, dim3(256), 0, s, a);
+    case 5: return launch_pdl(fp8_combine_kernel<5>, grid, dim3(256), 0, s, a);
+    case 6: return launch_pdl(fp8_combine_kernel<6>, grid, dim3(256), 0, s, a);
+    case 7: return launch_pdl(fp8_combine_kernel<7>, grid, dim3(256), 0, s, a);
+    default: return launch_pdl(fp8_combine_kernel<8>, grid, dim3(256), 0, s, a);
+  }
 }
 
 }  // namespace moe

@@ -296,7 +296,9 @@ Layout make_layout(const moe_layer& L, int64_t T, Weights kind = W_NATIVE) {
       w.ksplit = sp.g2.ksplit;
     }
   }
-  w.Yp = take(yp_rows > 0 ? sizeof(float) * static_cast<size_t>(yp_rows) * L.d : 0);
+  // (an 8-bit layer's scaled fp16 rows and their scales take less than fp32 rows
+  // from d = 16 on, but for the alignment between them)
+  w.Yp = take(yp_rows > 0 ? sizeof(float) * static_cast<size_t>(yp_rows) * L.d + (fp8 ? 256 : 0) : 0);
   w.P = take(p_bytes);
   w.Xq = take(fp8 ? static_cast<size_t>(T) * fp8_x_pitch(L) : 0);
   w.Hs = take(fp8 ? sizeof(float) * static_cast<size_t>(w.s_max) * ((L.d_ff + F8_GROUP - 1) / F8_GROUP) : 0);
@@ -679,6 +681,7 @@ int forward_impl(moe_handle h, int64_t T, const void* x, const float* W_r, const
   W4Plan wplan1, wplan2;
   W4SmallPlan splan1, splan2;
   Fp8Plan fplan1, fplan2;
+  bool h16 = false;  // 8-bit weights: the second projection's rows in scaled fp16
   if (fp8) {
     const char* why = nullptr;
     const int64_t pitch = fp8_x_pitch(L), hb = (L.d_ff + F8_GROUP - 1) / F8_GROUP;
@@ -733,6 +736,17 @@ int forward_impl(moe_handle h, int64_t T, const void* x, const float* W_r, const
     a2.ksplit = w.ksplit;
     a2.split_stride = static_cast<int64_t>(w.s_max) * L.d;
     a2.row_gate = r.row_gate;
+    // Batches of over 64 tokens whose K is not cut: the gated rows in fp16 with
+    // a power of two for each 128 columns.  That rounds each to 12 bits (half a
+    // unit 2^-12, against y's own 2^-9), and halves the bytes that lie between
+    // the second projection and the combine, which bind both where d_ff is
+    // small (16384 tokens, 128 experts of d_ff 768, top-4: see the layer's figures).
+    h16 = T > 64 && w.ksplit == 1;
+    if (h16) {
+      a2.epi = FP8_GATE_H16;
+      a2.out_scales = reinterpret_cast<float*>(ws + w.Yp + align256(sizeof(uint16_t) * static_cast<size_t>(w.s_max) * L.d));
+      a2.split_stride = 0;
+    }
     if (plan_fp8(a1, &fplan1, &why) != cudaSuccess || plan_fp8(a2, &fplan2, &why) != cudaSuccess)
       return fail(MOE_ERR_UNSUPPORTED, F + (why ? why : "8-bit product plan failed"));
   } else if (w4) {
@@ -891,7 +905,23 @@ int forward_impl(moe_handle h, int64_t T, const void* x, const float* W_r, const
                 : launch_gemm_simt(g2, w.s_max, s);
   if ((rc = check(ce, "gemm2")) != MOE_OK) return rc;
   record(dbg, MOE_STAGE_GEMM2, 1, s);
-  if (w.need_yp) {
+  if (h16) {
+    record(dbg, MOE_STAGE_COMBINE, 0, s);
+    Fp8CombineArgs ca;
+    memset(&ca, 0, sizeof(ca));
+    ca.T = T;
+    ca.k = L.k;
+    ca.d = L.d;
+    ca.n_shared = L.n_shared;
+    ca.dest_row = r.dest_row;
+    ca.shared_base = r.offsets + L.E;
+    ca.Y = reinterpret_cast<const uint16_t*>(ws + w.Yp);
+    ca.scales = reinterpret_cast<const float*>(ws + w.Yp + align256(sizeof(uint16_t) * static_cast<size_t>(w.s_max) * L.d));
+    ca.y = y;
+    ca.y_f32 = dbg ? dbg->y_f32 : nullptr;
+    if ((rc = check(launch_fp8_combine(ca, s), "combine")) != MOE_OK) return rc;
+    record(dbg, MOE_STAGE_COMBINE, 1, s);
+  } else if (w.need_yp) {
     record(dbg, MOE_STAGE_COMBINE, 0, s);
     if ((rc = check(launch_combine(T, L.k, L.d, L.dtype == MOE_BF16, r.dest_row, L.n_shared, r.offsets + L.E,
                                    reinterpret_cast<const float*>(ws + w.Yp), w.ksplit,

@@ -87,6 +87,13 @@ def reference(w, inp, q):
         er = F.product_bound(hv, W2) + move @ np.abs(W2).T
         y[rows] += gate * yr
         tol[rows] += np.abs(gate) * er + np.abs(yr) * 2e-6 + np.abs(gate * yr) * 4 * ULP
+        if w.T > 64:
+            # a gated row may lie in fp16 between the second projection and the sum,
+            # 128 columns of it scaled so that the largest is at least 2^14: half a
+            # unit of 11 bits, or of the smallest number, 2^-25 of 2^14 at least
+            big = np.concatenate([np.repeat(np.abs(yr[:, c:c + 128]).max(1, keepdims=True), min(128, w.d - c), 1)
+                                  for c in range(0, w.d, 128)], 1)
+            tol[rows] += np.abs(gate * yr) * 2.0 ** -12 * 1.001 + np.abs(gate) * big * 2.0 ** -39
     return o, y, tol + np.abs(y) * 8 * ULP + 1e-30
 
 
