@@ -14,15 +14,15 @@ constexpr int kFp8MaxGroups = 256;
 
 // ------------------------------------------------------------ quantisation
 struct QuantFp8Args {
-  const void* x;        // [G][R][K], rows ldx elements apart, matrices gsx elements apart
+  const void* x;        // [G][R][K], rows ldx elements apart, matrices gsx = R ldx
   int x_is_bf16;
   int G, R, K;
   int64_t ldx, gsx;
   int block_rows;       // rows under one scale: 1 or 128
   int transpose;        // codes and scales of the transposed matrices [K][R]
-  uint8_t* codes;       // [G][R or K], rows ldc bytes apart, matrices gsc bytes apart
+  uint8_t* codes;       // [G][R or K], rows ldc bytes apart, matrices one after another (gsc bytes)
   int64_t ldc, gsc;
-  float* scales;        // rows lds floats apart, matrices gss floats apart
+  float* scales;        // rows lds floats apart, matrices one after another (gss floats)
   int64_t lds, gss;
 };
 cudaError_t launch_quantize_fp8(const QuantFp8Args& a, cudaStream_t s);

@@ -104,64 +104,86 @@ __device__ __forceinline__ void store8(uint8_t* dst, uint2 c, int n, bool vec) {
 
 // Groups of 128 elements of a row: 16 lanes per group, 8 elements per lane,
 // UNROLL groups of a team of 16 lanes in flight at once (one load of 16 bytes
-// per lane keeps 32 KB in flight per SM, too few for HBM's latency).
+// per lane keeps 32 KB in flight per SM, too few for HBM's latency).  A block
+// takes 16 x UNROLL consecutive groups.
 constexpr int UNROLL = 4;
 
 template <typename XT>
-__global__ void __launch_bounds__(256) quant_rows_kernel(const QuantFp8Args a, int kb_n, int vec_in, int vec_out) {
+__global__ void __launch_bounds__(256) quant_rows_kernel(const QuantFp8Args a, uint32_t rows, int kb_n, int step_rows,
+                                                         int step_groups, int vec_in, int vec_out) {
+  static_assert(UNROLL == 4, "a lane divides for one group in four");
   const int l = threadIdx.x & 15;
-  const uint32_t teams = gridDim.x * 16u;
-  const uint32_t items = static_cast<uint32_t>(a.G) * static_cast<uint32_t>(a.R) * static_cast<uint32_t>(kb_n);
-  const XT* x = static_cast<const XT*>(a.x);
+  // this team's first group; the next ones lie 16 groups = step_rows rows and step_groups groups on
+  const uint32_t i0 = blockIdx.x * (16u * UNROLL) + (threadIdx.x >> 4);
+  uint32_t r = i0 / static_cast<uint32_t>(kb_n);
+  int g = static_cast<int>(i0 - r * static_cast<uint32_t>(kb_n));
   // every lane runs every step: the shuffles need both teams of a warp
   Eight<XT> v[UNROLL];
-  int64_t dst[UNROLL], sc[UNROLL];
-  int left[UNROLL];  // elements from this lane's first one to the end of the row; 0: no group
+  uint8_t* dst[UNROLL];
+  int left[UNROLL];  // elements from this lane's first one to the end of the row; 0 or less: none
+  uint32_t my_row = 0;  // of the group that this lane divides for
+  int my_g = 0;
 #pragma unroll
   for (int u = 0; u < UNROLL; ++u) {
-    const uint32_t i = blockIdx.x * 16u + (threadIdx.x >> 4) + static_cast<uint32_t>(u) * teams;
-    const bool live = i < items;
-    const uint32_t row = live ? i / static_cast<uint32_t>(kb_n) : 0u;
-    const uint32_t g = live ? i - row * static_cast<uint32_t>(kb_n) : 0u;
-    const uint32_t mat = a.G == 1 ? 0u : row / static_cast<uint32_t>(a.R), r = row - mat * static_cast<uint32_t>(a.R);
-    const int c = static_cast<int>(g) * F8_GROUP + l * 8;
+    const bool live = r < rows;
+    const int c = g * F8_GROUP + l * 8;
     left[u] = live ? a.K - c : 0;
-    dst[u] = static_cast<int64_t>(mat) * a.gsc + static_cast<int64_t>(r) * a.ldc + c;
-    sc[u] = static_cast<int64_t>(mat) * a.gss + static_cast<int64_t>(r) * a.lds + g;
-    v[u] = load8(x + static_cast<int64_t>(mat) * a.gsx + static_cast<int64_t>(r) * a.ldx, c, live ? a.K : 0, vec_in);
+    dst[u] = a.codes + static_cast<int64_t>(r) * a.ldc + c;
+    v[u] = load8(static_cast<const XT*>(a.x) + static_cast<int64_t>(live ? r : 0u) * a.ldx, c, live ? a.K : 0, vec_in);
+    if ((l & 3) == u) {
+      my_row = r;
+      my_g = g;
+    }
+    r += static_cast<uint32_t>(step_rows);
+    g += step_groups;
+    if (g >= kb_n) {
+      g -= kb_n;
+      ++r;
+    }
   }
+  float m[UNROLL];
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) m[u] = v[u].amax();
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], o));
+  // two divisions a lane, not eight: lane l of a team divides for group l & 3
+  const Fp8Scale q = fp8_scale((l & 2) ? ((l & 1) ? m[3] : m[2]) : ((l & 1) ? m[1] : m[0]));
+  if (l < UNROLL && my_row < rows) a.scales[static_cast<int64_t>(my_row) * a.lds + my_g] = q.scale;
 #pragma unroll
   for (int u = 0; u < UNROLL; ++u) {
-    float m = v[u].amax();
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const Fp8Scale q = fp8_scale(m);
-    store8(a.codes + dst[u], codes8(v[u], q.inv), left[u], vec_out);
-    if (l == 0 && left[u] > 0) a.scales[sc[u]] = q.scale;
+    const float inv = __shfl_sync(0xffffffffu, q.inv, (threadIdx.x & 16) + u);
+    store8(dst[u], codes8(v[u], inv), left[u], vec_out);
   }
 }
 
-// One 128 x 128 tile of a matrix per CTA: thread (ty, tx) holds rows ty + 16 j
-// and columns 8 tx .. 8 tx + 7.  BLOCK: one scale for the tile; else (the
+// One 128 x 128 tile of a matrix per CTA: thread (ty, tx) holds rows 8 ty .. 8 ty
+// + 7 and columns 8 tx .. 8 tx + 7.  BLOCK: one scale for the tile; else (the
 // transposed matrix in groups along its rows) one for each column of the tile.
+// TR: the codes go out transposed, through shared memory in units of 8 bytes
+// (8 rows of a column), unit u of column k at u ^ (k / 8) of the column's 128
+// bytes, so that neither side meets a bank twice.
 template <typename XT, bool BLOCK, bool TR>
 __global__ void __launch_bounds__(256) quant_tile_kernel(const QuantFp8Args a, int rb_n, int kb_n, int vec_in,
                                                          int vec_out) {
   static_assert(BLOCK || TR, "rows of an untransposed matrix take the row kernel");
-  __shared__ float s_red[BLOCK ? 8 : 16 * 128];
-  __shared__ alignas(16) uint8_t s_t[TR ? 128 * 144 : 16];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  __shared__ alignas(16) float s_red[BLOCK ? 8 : 8 * 128];
+  __shared__ alignas(16) float s_inv[BLOCK ? 4 : 128];
+  __shared__ alignas(16) uint8_t s_t[TR ? 128 * 128 : 16];
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, warp = threadIdx.x >> 5;
   const uint32_t per = static_cast<uint32_t>(rb_n) * static_cast<uint32_t>(kb_n);
   const uint32_t mat = blockIdx.x / per, tile = blockIdx.x - mat * per;
   const int rb = static_cast<int>(tile / static_cast<uint32_t>(kb_n));
   const int kb = static_cast<int>(tile - static_cast<uint32_t>(rb) * static_cast<uint32_t>(kb_n));
   const XT* x = static_cast<const XT*>(a.x) + static_cast<int64_t>(mat) * a.gsx;
-  const int c = kb * 128 + tx * 8;
+  float* scales = a.scales + static_cast<int64_t>(mat) * a.gss;
+  const int c = kb * 128 + tx * 8, r0 = rb * 128 + ty * 8;
   Eight<XT> v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int r = rb * 128 + ty + 16 * j;
-    v[j] = load8(x + static_cast<int64_t>(r) * a.ldx, c, r < a.R ? a.K : 0, vec_in);
+    const int r = r0 + j;
+    v[j] = load8(x + static_cast<int64_t>(r < a.R ? r : 0) * a.ldx, c, r < a.R ? a.K : 0, vec_in);
   }
   float inv[8];
   if (BLOCK) {
@@ -170,59 +192,63 @@ __global__ void __launch_bounds__(256) quant_tile_kernel(const QuantFp8Args a, i
     for (int j = 0; j < 8; ++j) m = fmaxf(m, v[j].amax());
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = m;
+    if ((threadIdx.x & 31) == 0) s_red[warp] = m;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = fmaxf(m, s_red[i]);
     const Fp8Scale q = fp8_scale(m);
 #pragma unroll
     for (int i = 0; i < 8; ++i) inv[i] = q.inv;
-    if (threadIdx.x == 0)
-      a.scales[static_cast<int64_t>(mat) * a.gss + (TR ? kb * a.lds + rb : rb * a.lds + kb)] = q.scale;
+    if (threadIdx.x == 0) scales[TR ? kb * a.lds + rb : rb * a.lds + kb] = q.scale;
   } else {
+    float m[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float m = fabsf(v[0].at(i));
+      m[i] = fabsf(v[0].at(i));
 #pragma unroll
-      for (int j = 1; j < 8; ++j) m = fmaxf(m, fabsf(v[j].at(i)));
-      s_red[ty * 128 + tx * 8 + i] = m;
+      for (int j = 1; j < 8; ++j) m[i] = fmaxf(m[i], fabsf(v[j].at(i)));
+      m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 16));
+    }
+    if ((threadIdx.x & 16) == 0) {
+      float4* red = reinterpret_cast<float4*>(s_red + warp * 128 + tx * 8);
+      red[0] = make_float4(m[0], m[1], m[2], m[3]);
+      red[1] = make_float4(m[4], m[5], m[6], m[7]);
     }
     __syncthreads();
+    if (threadIdx.x < 128) {  // a column each
+      float t = s_red[threadIdx.x];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float m = s_red[tx * 8 + i];
-#pragma unroll
-      for (int t = 1; t < 16; ++t) m = fmaxf(m, s_red[t * 128 + tx * 8 + i]);
-      const Fp8Scale q = fp8_scale(m);
-      inv[i] = q.inv;
-      if (ty == 0 && c + i < a.K) a.scales[static_cast<int64_t>(mat) * a.gss + static_cast<int64_t>(c + i) * a.lds + rb] = q.scale;
+      for (int w = 1; w < 8; ++w) t = fmaxf(t, s_red[w * 128 + threadIdx.x]);
+      const Fp8Scale q = fp8_scale(t);
+      s_inv[threadIdx.x] = q.inv;
+      const int k = kb * 128 + threadIdx.x;
+      if (k < a.K) scales[static_cast<int64_t>(k) * a.lds + rb] = q.scale;
     }
+    __syncthreads();
+    const float4* in = reinterpret_cast<const float4*>(s_inv + tx * 8);
+    const float4 lo = in[0], hi = in[1];
+    inv[0] = lo.x; inv[1] = lo.y; inv[2] = lo.z; inv[3] = lo.w;
+    inv[4] = hi.x; inv[5] = hi.y; inv[6] = hi.z; inv[7] = hi.w;
   }
   uint8_t* codes = a.codes + static_cast<int64_t>(mat) * a.gsc;
   if (!TR) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int r = rb * 128 + ty + 16 * j;
-      if (r < a.R) store8(codes + static_cast<int64_t>(r) * a.ldc + c, codes8(v[j], inv[0]), a.K - c, vec_out);
-    }
+    for (int j = 0; j < 8; ++j)
+      if (r0 + j < a.R) store8(codes + static_cast<int64_t>(r0 + j) * a.ldc + c, codes8(v[j], inv[0]), a.K - c, vec_out);
   } else {
-    // through shared memory: row k of the tile's transpose, 144 bytes apart
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        const uint32_t w = e4m3x2(v[j].at(i) * inv[i], v[j + 1].at(i) * inv[i]);
-        s_t[(tx * 8 + i) * 144 + ty + 16 * j] = static_cast<uint8_t>(w);
-        s_t[(tx * 8 + i) * 144 + ty + 16 * (j + 1)] = static_cast<uint8_t>(w >> 8);
-      }
+      const uint2 w = make_uint2(e4m3x4(v[0].at(i) * inv[i], v[1].at(i) * inv[i], v[2].at(i) * inv[i], v[3].at(i) * inv[i]),
+                                 e4m3x4(v[4].at(i) * inv[i], v[5].at(i) * inv[i], v[6].at(i) * inv[i], v[7].at(i) * inv[i]));
+      *reinterpret_cast<uint2*>(s_t + (tx * 8 + i) * 128 + ((ty ^ tx) << 3)) = w;
     }
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int k = ty + 16 * j, r = rb * 128 + tx * 8;
       if (kb * 128 + k < a.K)
-        store8(codes + static_cast<int64_t>(kb * 128 + k) * a.ldc + r, *reinterpret_cast<const uint2*>(s_t + k * 144 + tx * 8),
-               a.R - r, vec_out);
+        store8(codes + static_cast<int64_t>(kb * 128 + k) * a.ldc + r,
+               *reinterpret_cast<const uint2*>(s_t + k * 128 + ((tx ^ (k >> 3)) << 3)), a.R - r, vec_out);
     }
   }
 }
@@ -236,9 +262,11 @@ cudaError_t launch_x(const QuantFp8Args& a, cudaStream_t s) {
   const int vec_out = ((reinterpret_cast<uintptr_t>(a.codes) | static_cast<uintptr_t>(a.ldc) |
                         static_cast<uintptr_t>(a.gsc)) & 7) == 0;
   if (a.block_rows == 1 && !a.transpose) {
-    const int64_t items = static_cast<int64_t>(a.G) * a.R * kb;  // below 2^31
+    // (matrices lie one after another, so their rows are rows of one)
+    const int64_t rows = static_cast<int64_t>(a.G) * a.R, items = rows * kb;  // below 2^31
     const int64_t blocks = (items + 16 * UNROLL - 1) / (16 * UNROLL);
-    quant_rows_kernel<XT><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a, kb, vec_in, vec_out);
+    quant_rows_kernel<XT><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a, static_cast<uint32_t>(rows), kb, 16 / kb,
+                                                                       16 % kb, vec_in, vec_out);
   } else {
     const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.G) * rb * kb);
     if (a.block_rows == 128) {
