@@ -52,16 +52,7 @@ int common(const std::string& F, int64_t T, int E, int k, const void* logits, in
   return MOE_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t moe_router_balance_workspace_bytes(int64_t T, int num_experts, int64_t sequences) {
-  if (T < 0 || num_experts < 1 || num_experts > kBalanceMaxE || sequences < 0) return 0;
-  return balance_workspace_bytes(T, num_experts, sequences);
-}
-
-int moe_router_balance(int64_t T, int num_experts, int k, const void* logits, int dtype, int scoring, int64_t sequences,
+int router_balance(int64_t T, int num_experts, int k, const void* logits, int dtype, int scoring, int64_t sequences,
                        const int32_t* offsets, const uint8_t* mask, float* aux, float* z, int32_t* counts,
                        int32_t* tokens, void* workspace, size_t workspace_bytes, void* stream) {
   const std::string F = "moe_router_balance: ";
@@ -89,7 +80,7 @@ int moe_router_balance(int64_t T, int num_experts, int k, const void* logits, in
   return done();
 }
 
-int moe_router_balance_backward(int64_t T, int num_experts, int k, const void* logits, int dtype, int scoring,
+int router_balance_backward(int64_t T, int num_experts, int k, const void* logits, int dtype, int scoring,
                                 int64_t sequences, const int32_t* offsets, const uint8_t* mask, const int32_t* counts,
                                 const int32_t* tokens, const float* daux, const float* dz, float* dlogits,
                                 void* stream) {
@@ -115,6 +106,39 @@ int moe_router_balance_backward(int64_t T, int num_experts, int k, const void* l
   }
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, F + cudaGetErrorString(e));
   return done();
+}
+
+}  // namespace
+
+// No C++ exception (a message that finds no memory) leaves a C entry.
+extern "C" {
+
+size_t moe_router_balance_workspace_bytes(int64_t T, int num_experts, int64_t sequences) {
+  if (T < 0 || num_experts < 1 || num_experts > kBalanceMaxE || sequences < 0) return 0;
+  return balance_workspace_bytes(T, num_experts, sequences);
+}
+
+int moe_router_balance(int64_t T, int num_experts, int k, const void* logits, int dtype, int scoring, int64_t sequences,
+                       const int32_t* offsets, const uint8_t* mask, float* aux, float* z, int32_t* counts,
+                       int32_t* tokens, void* workspace, size_t workspace_bytes, void* stream) {
+  try {
+    return router_balance(T, num_experts, k, logits, dtype, scoring, sequences, offsets, mask, aux, z, counts, tokens,
+                          workspace, workspace_bytes, stream);
+  } catch (...) {
+    return MOE_ERR_CUDA;
+  }
+}
+
+int moe_router_balance_backward(int64_t T, int num_experts, int k, const void* logits, int dtype, int scoring,
+                                int64_t sequences, const int32_t* offsets, const uint8_t* mask, const int32_t* counts,
+                                const int32_t* tokens, const float* daux, const float* dz, float* dlogits,
+                                void* stream) {
+  try {
+    return router_balance_backward(T, num_experts, k, logits, dtype, scoring, sequences, offsets, mask, counts, tokens,
+                                   daux, dz, dlogits, stream);
+  } catch (...) {
+    return MOE_ERR_CUDA;
+  }
 }
 
 }  // extern "C"

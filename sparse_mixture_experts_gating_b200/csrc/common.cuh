@@ -128,8 +128,9 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, uint64_t
       : "memory");
 }
 
-// Store of one box of a 3D tensor from shared memory (the box's columns past
-// the tensor's end are left out), in the thread's current bulk group.
+// Store of one box of a 3D tensor from shared memory, in the thread's current
+// bulk group.  The box's rows past the tensor's end are left out, its columns in
+// whole 16-byte pieces (77 fp32 columns were written as 80).
 __device__ __forceinline__ void tma_store_3d(const void* map, const void* src, int x, int y, int z) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),

@@ -101,6 +101,7 @@ struct Fp8ReduceArgs {
   const float* P;
   int ksplit;
   int64_t split_stride, rows;
+  int64_t ld;    // floats between rows of a partial, a multiple of 4
   int N;
   void* out;
   int out_is_bf16;

@@ -28,11 +28,10 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-}  // namespace
+// Floats between the rows of a partial: whole 16-byte pieces.
+int64_t partial_ld(int64_t N) { return (N + 3) / 4 * 4; }
 
-extern "C" {
-
-int moe_quantize_fp8(const void* x, int dtype, int64_t matrices, int64_t rows, int64_t K, int64_t ld, int block_rows,
+int quantize_fp8(const void* x, int dtype, int64_t matrices, int64_t rows, int64_t K, int64_t ld, int block_rows,
                      int transpose, void* codes, int64_t ld_codes, float* scales, void* stream) {
   const std::string F = "moe_quantize_fp8: ";
   if (matrices < 0 || rows < 0 || K < 0) return fail(MOE_ERR_INVALID_ARG, F + "matrices, rows or K < 0");
@@ -41,7 +40,7 @@ int moe_quantize_fp8(const void* x, int dtype, int64_t matrices, int64_t rows, i
   if (matrices == 0 || rows == 0 || K == 0) return done();
   const int64_t out_rows = transpose ? K : rows, out_cols = transpose ? rows : K;
   if (ld < K || ld_codes < out_cols) return fail(MOE_ERR_INVALID_ARG, F + "a row stride is smaller than its row");
-  if (rows > 2147483647LL || K > 2147483647LL || ld > (int64_t{1} << 40) || ld_codes > (int64_t{1} << 40))
+  if (rows > (int64_t{1} << 30) || K > (int64_t{1} << 30) || ld > (int64_t{1} << 32) || ld_codes > (int64_t{1} << 32))
     return fail(MOE_ERR_UNSUPPORTED, F + "rows, K or a row stride is too large");
   // groups (or tiles) are counted in 31 bits
   const int64_t per = block_rows == 1 && !transpose ? rows * ceil_div(K, F8_GROUP)
@@ -73,17 +72,9 @@ int moe_quantize_fp8(const void* x, int dtype, int64_t matrices, int64_t rows, i
   return done();
 }
 
-size_t moe_matmul_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t groups) {
-  if (M <= 0 || N <= 0 || K <= 0 || groups <= 0 || groups > kFp8MaxGroups || N > 2147483647LL || K > 2147483647LL)
-    return 0;
-  const int ks = fp8_ksplit(M, static_cast<int>(groups), static_cast<int>(N), static_cast<int>(K));
-  return ks > 1 ? sizeof(float) * static_cast<size_t>(ks) * static_cast<size_t>(M) * static_cast<size_t>(N) : 0;
-}
-
-int moe_matmul_fp8(int64_t M, int64_t N, int64_t K, int64_t groups, const void* a_codes, int64_t lda,
-                   const float* a_scales, const void* b_codes, int64_t ldb, const float* b_scales, int b_rows,
-                   const int32_t* offsets, void* out, int out_dtype, int64_t ld_out, void* workspace,
-                   size_t workspace_bytes, void* stream) {
+int matmul_fp8(int64_t M, int64_t N, int64_t K, int64_t groups, const void* a_codes, int64_t lda, const float* a_scales,
+               const void* b_codes, int64_t ldb, const float* b_scales, int b_rows, const int32_t* offsets, void* out,
+               int out_dtype, int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream) {
   const std::string F = "moe_matmul_fp8: ";
   if (M < 0 || N < 1 || K < 1) return fail(MOE_ERR_INVALID_ARG, F + "need M >= 0, N >= 1 and K >= 1");
   if (groups < 1 || groups > kFp8MaxGroups) return fail(MOE_ERR_INVALID_ARG, F + "groups must be in [1, 256]");
@@ -129,9 +120,9 @@ int moe_matmul_fp8(int64_t M, int64_t N, int64_t K, int64_t groups, const void* 
   a.sb0 = b_scales;
   a.b_rows = b_rows;
   a.out = ks > 1 ? workspace : out;
-  a.ld_out = ks > 1 ? N : ld_out;
+  a.ld_out = ks > 1 ? partial_ld(N) : ld_out;
   a.ksplit = ks;
-  a.split_stride = ks > 1 ? M * N : 0;
+  a.split_stride = ks > 1 ? M * partial_ld(N) : 0;
   a.offsets = offsets;
   a.err = err;
   Fp8Plan plan;
@@ -144,7 +135,8 @@ int moe_matmul_fp8(int64_t M, int64_t N, int64_t K, int64_t groups, const void* 
     memset(&r, 0, sizeof(r));
     r.P = static_cast<const float*>(workspace);
     r.ksplit = ks;
-    r.split_stride = M * N;
+    r.split_stride = M * partial_ld(N);
+    r.ld = partial_ld(N);
     r.rows = M;
     r.N = static_cast<int>(N);
     r.out = out;
@@ -156,6 +148,38 @@ int moe_matmul_fp8(int64_t M, int64_t N, int64_t K, int64_t groups, const void* 
   }
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, F + cudaGetErrorString(e));
   return done();
+}
+}  // namespace
+
+// No C++ exception (a message that finds no memory) leaves a C entry.
+extern "C" {
+
+int moe_quantize_fp8(const void* x, int dtype, int64_t matrices, int64_t rows, int64_t K, int64_t ld, int block_rows,
+                     int transpose, void* codes, int64_t ld_codes, float* scales, void* stream) {
+  try {
+    return quantize_fp8(x, dtype, matrices, rows, K, ld, block_rows, transpose, codes, ld_codes, scales, stream);
+  } catch (...) {
+    return MOE_ERR_CUDA;
+  }
+}
+
+size_t moe_matmul_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t groups) {
+  if (M <= 0 || N <= 0 || K <= 0 || groups <= 0 || groups > kFp8MaxGroups || N > 2147483647LL || K > 2147483647LL)
+    return 0;
+  const int ks = fp8_ksplit(M, static_cast<int>(groups), static_cast<int>(N), static_cast<int>(K));
+  return ks > 1 ? sizeof(float) * static_cast<size_t>(ks) * static_cast<size_t>(M) * static_cast<size_t>(partial_ld(N)) : 0;
+}
+
+int moe_matmul_fp8(int64_t M, int64_t N, int64_t K, int64_t groups, const void* a_codes, int64_t lda,
+                   const float* a_scales, const void* b_codes, int64_t ldb, const float* b_scales, int b_rows,
+                   const int32_t* offsets, void* out, int out_dtype, int64_t ld_out, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  try {
+    return matmul_fp8(M, N, K, groups, a_codes, lda, a_scales, b_codes, ldb, b_scales, b_rows, offsets, out, out_dtype,
+                      ld_out, workspace, workspace_bytes, stream);
+  } catch (...) {
+    return MOE_ERR_CUDA;
+  }
 }
 
 }  // extern "C"

@@ -672,9 +672,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 }
 
 // ---------------------------------------------------------------- partials
-// Thread: four columns of a row (VEC: as one 16-byte access), every partial in
-// order; eight partials' loads in flight.
-template <bool BF16, bool VEC>
+// Thread: four columns of a row (one 16-byte access; the partials' rows are
+// padded to whole ones), every partial in order; eight partials' loads in
+// flight.
+template <bool BF16>
 __global__ void __launch_bounds__(128) fp8_reduce_kernel(const Fp8ReduceArgs a) {
   __shared__ int s_last;
   pdl_wait();
@@ -692,7 +693,7 @@ __global__ void __launch_bounds__(128) fp8_reduce_kernel(const Fp8ReduceArgs a) 
   const int c0 = (blockIdx.x * 128 + threadIdx.x) * 4;
   if (c0 >= a.N) return;
   for (int64_t r = r0 + blockIdx.y; r < r1; r += gridDim.y) {
-    const float* src = a.P + r * a.N + c0;
+    const float* src = a.P + r * a.ld + c0;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     for (int k0 = 0; k0 < a.ksplit; k0 += 8) {
       float4 q[8];
@@ -700,16 +701,7 @@ __global__ void __launch_bounds__(128) fp8_reduce_kernel(const Fp8ReduceArgs a) 
       for (int u = 0; u < 8; ++u) {
         const float* s = src + (k0 + u) * a.split_stride;
         q[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k0 + u < a.ksplit) {
-          if (VEC) {
-            q[u] = *reinterpret_cast<const float4*>(s);
-          } else {
-            q[u].x = s[0];
-            if (c0 + 1 < a.N) q[u].y = s[1];
-            if (c0 + 2 < a.N) q[u].z = s[2];
-            if (c0 + 3 < a.N) q[u].w = s[3];
-          }
-        }
+        if (k0 + u < a.ksplit) q[u] = *reinterpret_cast<const float4*>(s);
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u) { v[0] += q[u].x; v[1] += q[u].y; v[2] += q[u].z; v[3] += q[u].w; }
@@ -922,17 +914,20 @@ cudaError_t plan_fp8(const Fp8Args& g, Fp8Plan* pl, const char** why) {
   p.pair_stride = g.pair_stride;
   p.out_scales = g.out_scales;
   const int elt = g.epi == FP8_BF16 || g.epi == FP8_GATE_H16 ? 2 : 4;
+  // (a partial's rows have room behind N for the last piece)
+  const bool whole_n = g.epi == FP8_F32 && p.ksplit > 1 && g.ld_out >= (g.N + 3) / 4 * 4;
   p.vec_out = ((reinterpret_cast<uintptr_t>(g.out) | static_cast<uintptr_t>(g.ld_out * elt) |
-                static_cast<uintptr_t>(static_cast<int64_t>(g.N) * elt) | static_cast<uintptr_t>(g.split_stride * elt) |
+                static_cast<uintptr_t>(whole_n ? 0 : static_cast<int64_t>(g.N) * elt) | static_cast<uintptr_t>(g.split_stride * elt) |
                 static_cast<uintptr_t>(g.pair_stride * elt)) & 15) == 0;
-  // whole tiles of the output by TMA, where its rows allow it
+  // whole tiles of the output by TMA, where its rows allow it (a store is cut off at
+  // the row's end in whole 16-byte pieces only)
   const bool act = g.epi == FP8_SWIGLU || g.epi == FP8_RELU;
   const int oelt = act ? 1 : elt;
   p.tma_out = 0;
   pl->out = pl->a;
   if (pl->ar == 128 && g.epi != FP8_PAIR_F32 &&
       ((reinterpret_cast<uintptr_t>(g.out) | static_cast<uintptr_t>(g.ld_out * oelt) |
-        static_cast<uintptr_t>(g.split_stride * oelt)) & 15) == 0) {
+        static_cast<uintptr_t>(whole_n ? 0 : static_cast<int64_t>(g.N) * oelt) | static_cast<uintptr_t>(g.split_stride * oelt)) & 15) == 0) {
     const CUtensorMapDataType type = act ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                          : g.epi == FP8_GATE_H16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                          : elt == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
@@ -963,12 +958,8 @@ cudaError_t launch_fp8(const Fp8Plan& pl, int num_sms, cudaStream_t s) {
 cudaError_t launch_fp8_reduce(const Fp8ReduceArgs& a, cudaStream_t s) {
   if (a.rows <= 0 || a.N <= 0) return cudaSuccess;
   const dim3 grid(static_cast<unsigned>((a.N + 511) / 512), static_cast<unsigned>(std::min<int64_t>(a.rows, 65535)));
-  const bool vec = a.N % 4 == 0;  // (partials are 256-byte aligned and N floats apart)
-  if (a.out_is_bf16)
-    return vec ? launch_pdl(fp8_reduce_kernel<true, true>, grid, dim3(128), 0, s, a)
-               : launch_pdl(fp8_reduce_kernel<true, false>, grid, dim3(128), 0, s, a);
-  return vec ? launch_pdl(fp8_reduce_kernel<false, true>, grid, dim3(128), 0, s, a)
-             : launch_pdl(fp8_reduce_kernel<false, false>, grid, dim3(128), 0, s, a);
+  return a.out_is_bf16 ? launch_pdl(fp8_reduce_kernel<true>, grid, dim3(128), 0, s, a)
+                       : launch_pdl(fp8_reduce_kernel<false>, grid, dim3(128), 0, s, a);
 }
 
 cudaError_t launch_fp8_hidden(const Fp8HiddenArgs& a, int num_sms, cudaStream_t s) {

@@ -233,8 +233,8 @@ class MoELayer:
                          W_r.new_empty(1), W_r.new_empty(1))
             counts, dropped, aux, z = stats
             if workspace is None:
-                workspace = W_r.new_empty(max(self.workspace_bytes_fp8(T), 256), dtype=torch.uint8)
-                self._last = workspace
+                self._last = None  # (let go of the last call's before asking for this one's)
+                workspace = self._last = W_r.new_empty(max(self.workspace_bytes_fp8(T), 256), dtype=torch.uint8)
             dbg = _debug_struct(debug, events, stream)
             q3, s3 = (None, None) if W3q is None else W3q
             check(lib().moe_forward_fp8(

@@ -200,3 +200,59 @@ def test_with_the_layer():
         assert (own[name] - without[name]).abs().max() > 1e-3 * scale, name  # the losses do reach it
     for name in ("dW1", "dW2"):
         assert torch.equal(own[name], ours[name])
+
+
+def test_offsets_out_of_order_stay_inside():
+    """Offsets that leave [0, T] or do not ascend: whatever the sums are, nothing
+    outside the results is written, and a gradient is written for every token."""
+    T, E, k = 500, 12, 3
+    l, _ = make(T, E, 6, F32, False, False)
+    one = torch.ones(3, device="cuda")
+    for cuts in ([-5, 100, 50, 900], [400, 300, 200, 100], [0, 2 ** 31 - 1, -2 ** 31, 500]):
+        off = torch.tensor(cuts, dtype=torch.int64).to(torch.int32).cuda()
+        aux, z, counts, tokens, d = run(l, k, off, None, "softmax", one, one)
+        status()
+        assert d.shape == (T, E)
+
+
+def test_captured_and_replayed_and_on_another_stream():
+    l, m = make(2000, 40, 9, F32, True, False)
+    off = torch.tensor([0, 700, 2000], dtype=torch.int32, device="cuda")
+    g2 = torch.ones(2, device="cuda")
+    first = run(l, 4, off, m, "sigmoid", g2, g2)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = run(l, 4, off, m, "sigmoid", g2, g2)
+    g.replay()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = run(l, 4, off, m, "sigmoid", g2, g2, stream=s)
+    torch.cuda.synchronize()
+    for a, b, c in zip(first, out, other):
+        assert torch.equal(a, b) and torch.equal(a, c)
+    l.copy_(l.flip(1))  # (NaN where padding stood, still)
+    g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(out, run(l, 4, off, m, "sigmoid", g2, g2)):
+        assert torch.equal(a, b)
+
+
+def test_binding_refusals():
+    l, _ = make(10, 6, 3, F32, False, False)
+    off = torch.tensor([0, 10], dtype=torch.int32, device="cuda")
+    c, t = torch.zeros((1, 6), dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    for call in (lambda: router_balance(l.half(), 2), lambda: router_balance(l[:, ::2], 2), lambda: router_balance(l[0], 2),
+                 lambda: router_balance(l, 2, offsets=off.long()), lambda: router_balance(l, 2, offsets=off[:0]),
+                 lambda: router_balance(l, 2, mask=torch.ones(9, dtype=torch.bool, device="cuda")),
+                 lambda: router_balance(l, 2, scoring="relu"), lambda: router_balance(l, 2, offsets=off.cpu()),
+                 lambda: router_balance_backward(l, c[:, :5], t, None, None, 2),
+                 lambda: router_balance_backward(l, c, t, torch.ones(2, device="cuda"), None, 2)):
+        with pytest.raises(ValueError):
+            call()
+    from sparse_mixture_experts_gating_b200 import MoEError
+    for k in (0, 7, 9):
+        with pytest.raises(MoEError):
+            router_balance(l, k)
+    d = router_balance_backward(l, c, t, None, None, 2)
+    assert not d.any()

@@ -141,3 +141,159 @@ def test_grouped_product(M, N, K, cuts, out_dtype):
             check_product(out[lo:hi], av[lo:hi], host((b[0][g], b[1][g]), 128), out_dtype)
     outside = torch.cat([out[: cuts[0]], out[cuts[-1]:]])
     assert (outside == 7.0).all()
+
+
+def test_product_writes_its_columns_only():
+    """A result with a wider row stride, and one that starts at an odd element."""
+    a, b = operands(140, 77, 256, None, 128, 5)
+    for dtype in (BF, F32):
+        for first in (0, 1, 8):
+            big = torch.full((140, 100), 3.0, dtype=dtype, device="cuda")
+            out = big[:, first:first + 77]
+            matmul_fp8(a, b, out=out, out_dtype=dtype)
+            status()
+            check_product(out, host(a, 1), host(b, 128), dtype)
+            assert (big[:, :first] == 3).all() and (big[:, first + 77:] == 3).all()
+
+
+def test_product_with_zero_and_tiny_scales_and_not_a_number():
+    M, N, K = 40, 130, 256
+    x = torch.randn((M, K), device="cuda", generator=gen(1))
+    w = torch.randn((N, K), device="cuda", generator=gen(2))
+    x[3] = 0.0
+    w[:, 128:] = 0.0
+    x[5] *= 1e-20
+    x[7, 9] = float("nan")
+    a, b = quantize_fp8(x), quantize_fp8(w, block_rows=128)
+    y = matmul_fp8(a, b, out_dtype=F32)
+    status()
+    assert not y[3].any() and torch.isnan(y[7]).all()
+    keep = [i for i in range(M) if i != 7]
+    av = host(a, 1)[keep]
+    check_product(y[keep], av, host(b, 128), F32)
+
+
+@pytest.mark.parametrize("M", [50, 400])
+def test_offsets_out_of_order_stay_inside(M):
+    """Offsets that do not ascend or leave [0, M] are clamped and made ascending:
+    the rows outside the clamped range are left alone, the buffer's end too."""
+    G, N, K = 4, 64, 128
+    a, b = operands(M, N, K, G, 128, 3)
+    big = torch.full((M + 64, N), 5.0, device="cuda")
+    for cuts in ([10, 5, 30, 20, 40], [-7, 3, 1000000, 12, 20], [20, 20, 10, 10, 30]):
+        big.fill_(5.0)
+        matmul_fp8(a, b, offsets=torch.tensor(cuts, dtype=torch.int32, device="cuda"), out=big[:M], out_dtype=F32)
+        status()
+        run = np.clip(np.maximum.accumulate(np.clip(cuts, 0, M)), 0, M)
+        av = host(a, 1)
+        for g in range(G):
+            if run[g + 1] > run[g]:
+                check_product(big[run[g]:run[g + 1]], av[run[g]:run[g + 1]], host((b[0][g], b[1][g]), 128), F32)
+        assert (big[:run[0]] == 5).all() and (big[run[-1]:] == 5).all()
+
+
+def test_the_three_products_of_a_linear_layer():
+    """y = x W^T, dx = dy W and dW = dy^T x on the quantiser's plain and transposed
+    forms, against the same products of the numbers they stand for."""
+    T, d_in, d_out = 300, 200, 330
+    x = torch.randn((T, d_in), device="cuda", generator=gen(1)).to(BF)
+    W = torch.randn((d_out, d_in), device="cuda", generator=gen(2)).to(BF) * d_in ** -0.5
+    dy = torch.randn((T, d_out), device="cuda", generator=gen(3)).to(BF)
+    xq, Wq, dyq = quantize_fp8(x), quantize_fp8(W, block_rows=128), quantize_fp8(dy)
+    Wt = quantize_fp8(W, block_rows=128, transpose=True)
+    xt, dyt = quantize_fp8(x, transpose=True), quantize_fp8(dy, transpose=True)
+    # a weight's blocks are square: its transposed form stands for the same numbers
+    np.testing.assert_array_equal(host(Wt, 128), host(Wq, 128).T)
+    y = matmul_fp8(xq, Wq)
+    dx = matmul_fp8(dyq, Wt, out_dtype=F32)
+    dW = matmul_fp8(dyt, xt, out_dtype=F32)
+    status()
+    check_product(y, host(xq, 1), host(Wq, 128), BF)
+    check_product(dx, host(dyq, 1), host(Wt, 128), F32)
+    check_product(dW, host(dyt, 1), host(xt, 1), F32)
+    # and they are the layer's own within the format's rounding: half a step of 3
+    # bits, 2^-4, of each operand (2^-8 more for the two together and for bf16 y),
+    # or for numbers below the smallest normal code 2^-10 of a scale, 2^-10 / 448 of
+    # the block's largest, against at most 330 others: 7.2e-4 of both's largest
+    for got, p, q in ((y, x, W), (dx, dy, W.T), (dW, dy.T, x.T)):
+        p, q = p.double().cpu().numpy(), q.double().cpu().numpy()
+        tol = (2 * 2.0 ** -4 + 2.0 ** -8) * (np.abs(p) @ np.abs(q).T) + 2.0 ** -8 * np.abs(p @ q.T) + 1e-3 * np.abs(p).max() * np.abs(q).max()
+        assert (np.abs(got.double().cpu().numpy() - p @ q.T) <= tol).all()
+
+
+def test_on_another_stream_and_two_at_once():
+    a, b = operands(300, 512, 1024, None, 128, 8)
+    c, d = operands(1, 1024, 4096, None, 128, 9)
+    first, second = matmul_fp8(a, b), matmul_fp8(c, d)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (s1, s2):
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(8):
+        got.append((matmul_fp8(a, b, stream=s1), matmul_fp8(c, d, stream=s2)))
+    x = torch.randn((64, 512), device="cuda", generator=gen(4))
+    s1.wait_stream(torch.cuda.current_stream())
+    q = quantize_fp8(x, stream=s1)
+    torch.cuda.synchronize()
+    status()
+    for y, z in got:
+        assert torch.equal(y, first) and torch.equal(z, second)
+    check_quantized(x, *q, 1, False)
+
+
+def test_captured_and_replayed_on_new_inputs():
+    """quantise -> product -> quantise -> product in a graph, replayed on other inputs."""
+    x = torch.randn((130, 512), device="cuda", generator=gen(1)).to(BF)
+    w1 = quantize_fp8(torch.randn((1024, 512), device="cuda", generator=gen(2)) * 0.05, block_rows=128)
+    w2 = quantize_fp8(torch.randn((256, 1024), device="cuda", generator=gen(3)) * 0.05, block_rows=128)
+
+    def chain(x):
+        return matmul_fp8(quantize_fp8(matmul_fp8(quantize_fp8(x), w1)), w2)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        chain(x)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = chain(x)
+    for seed in (5, 6):
+        x.copy_(torch.randn((130, 512), device="cuda", generator=gen(seed)).to(BF))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, chain(x))
+    status()
+
+
+def test_binding_refusals():
+    a, b = operands(8, 64, 128, None, 128, 1)
+    g3 = operands(8, 64, 128, 2, 128, 1)[1]
+    off = torch.tensor([0, 4, 8], dtype=torch.int32, device="cuda")
+    bad = [
+        lambda: quantize_fp8(torch.zeros(4, device="cuda")),
+        lambda: quantize_fp8(torch.zeros((4, 4), dtype=torch.float16, device="cuda")),
+        lambda: quantize_fp8(torch.zeros((4, 4), device="cuda"), block_rows=64),
+        lambda: matmul_fp8(a, g3),
+        lambda: matmul_fp8(a, b, offsets=off),
+        lambda: matmul_fp8(a, g3, offsets=off.long()),
+        lambda: matmul_fp8(a, g3, offsets=off[:2]),
+        lambda: matmul_fp8(a, b, out_dtype=torch.float16),
+        lambda: matmul_fp8(a, b, out=torch.empty((8, 63), dtype=BF, device="cuda")),
+        lambda: matmul_fp8(a, b, out=torch.empty((8, 64), dtype=F32, device="cuda")),
+        lambda: matmul_fp8((a[0].view(torch.uint8), a[1]), b),
+        lambda: matmul_fp8((a[0], a[1].double()), b),
+        lambda: matmul_fp8((a[0], a[1].cpu()), b),
+        lambda: matmul_fp8((a[0][:, :64], a[1]), b),
+        lambda: matmul_fp8(a, (b[0], b[1][:, :0])),
+    ]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    from sparse_mixture_experts_gating_b200 import MoEError
+    with pytest.raises(MoEError, match="multiples of 16 bytes"):  # codes of another maker, rows 100 bytes apart
+        matmul_fp8((torch.zeros((8, 100), dtype=torch.float8_e4m3fn, device="cuda"), torch.ones((8, 1), device="cuda")),
+                   (torch.zeros((8, 100), dtype=torch.float8_e4m3fn, device="cuda"), torch.ones((1, 1), device="cuda")))
+    empty = matmul_fp8((a[0][:0], a[1][:0]), b)
+    assert empty.shape == (0, 64)
+    status()

@@ -131,3 +131,113 @@ def test_layer_matches_its_definition(w):
     inp = make_inputs(w, device="cuda")
     q = quantized(inp)
     check(w, inp, q, run(w, inp, q))
+
+
+CUT = [  # both projections with K cut: few rows, and whole 128-row tiles; scaled fp16 rows; many experts
+    Workload("cut_few_rows", T=3, d=2048, E=4, k=2, d_ff=128, act=S, gate=RN, capacity_factor=0.0, dtype=DTYPE_BF16,
+             dyadic=True, seed=41),
+    Workload("cut_first", T=100, d=2048, E=2, k=1, d_ff=256, act=S, gate=SW, capacity_factor=0.0, dtype=DTYPE_BF16,
+             dyadic=True, seed=42),
+    Workload("cut_second", T=100, d=128, E=2, k=2, d_ff=2048, act=R, gate=RN, capacity_factor=0.0, dtype=DTYPE_BF16,
+             dyadic=True, seed=43),
+    Workload("many_experts", T=260, d=64, E=200, k=8, d_ff=48, act=S, gate=RN, capacity_factor=0.0, dtype=DTYPE_BF16,
+             dyadic=True, seed=44),
+]
+
+
+@pytest.mark.parametrize("w", CUT, ids=lambda w: w.name)
+def test_cut_products_match_the_definition(w):
+    inp = make_inputs(w, device="cuda")
+    q = quantized(inp)
+    check(w, inp, q, run(w, inp, q))
+
+
+def test_layer_is_its_operators_in_a_row():
+    """One expert that every token takes with gate 1: the layer is quantise, product,
+    activation, quantise, product with the standalone operators."""
+    w = Workload("one_expert", T=200, d=256, E=1, k=1, d_ff=384, act=S, gate=RN, capacity_factor=0.0, dtype=DTYPE_BF16,
+                 dyadic=True, seed=51)
+    inp = make_inputs(w, device="cuda")
+    q = quantized(inp)
+    g = run(w, inp, q)
+    xq = quantize_fp8(inp["x"])
+    first = [(q[n][0][0], q[n][1][0]) for n in ("W1", "W3", "W2")]
+    a1, a3 = (matmul_fp8(xq, p, out_dtype=torch.float32) for p in first[:2])
+    h = torch.nn.functional.silu(a1) * a3
+    y = matmul_fp8(quantize_fp8(h), first[2], out_dtype=torch.float32)
+    status()
+    o, ref, tol = reference(w, inp, q)
+    assert (np.abs(y.double().cpu().numpy() - ref) <= tol).all()
+    assert (np.abs(g["y_f32"] - y.cpu().numpy()) <= 2 * tol).all()
+
+
+def test_same_inputs_give_the_same_bits_and_calls_share_nothing():
+    w = CASES[4]
+    inp = make_inputs(w, device="cuda")
+    q = quantized(inp)
+    layer = layer_for(w)
+    args = (inp["x"], inp["W_r"], inp["b_r"], q["W1"], q["W3"], q["W2"])
+    first = layer.forward_fp8(*args)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [layer.forward_fp8(*args, stream=s) for s in streams for _ in range(3)]
+    torch.cuda.synchronize()
+    status()
+    for r in got:
+        for a, b in zip(first, r):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("w", [CASES[1], CASES[4]], ids=lambda w: w.name)
+def test_layer_captured_and_replayed_beside_another_graph(w):
+    inp = make_inputs(w, device="cuda")
+    q = quantized(inp)
+    layer = layer_for(w)
+    x = inp["x"].clone()
+
+    def call():
+        return layer.forward_fp8(x, inp["W_r"], inp["b_r"], q["W1"], q["W3"], q["W2"])
+
+    call()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, call()))
+    x.copy_(inp["x"].flip(0))
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for s, (g, _) in zip((s1, s2), graphs):
+        with torch.cuda.stream(s):
+            for _ in range(4):
+                g.replay()
+    torch.cuda.synchronize()
+    ref = call()
+    torch.cuda.synchronize()
+    status()
+    for _, out in graphs:
+        for a, b in zip(out, ref):
+            assert torch.equal(a, b)
+
+
+def test_empty_batch_and_refusals():
+    w = CASES[1]
+    inp = make_inputs(w, device="cuda")
+    q = quantized(inp)
+    layer = layer_for(w)
+    y, counts, dropped, aux, z = layer.forward_fp8(inp["x"][:0], inp["W_r"], None, q["W1"], q["W3"], q["W2"])
+    status()
+    assert y.shape == (0, w.d) and not counts.any() and dropped.item() == 0 and aux.item() == 0 and z.item() == 0
+    x, W_r = inp["x"], inp["W_r"]
+    for call in (lambda: layer.forward_fp8(x.float(), W_r, None, q["W1"], q["W3"], q["W2"]),
+                 lambda: layer.forward_fp8(x[:, :128], W_r, None, q["W1"], q["W3"], q["W2"]),
+                 lambda: layer.forward_fp8(x, W_r, None, None, q["W3"], q["W2"]),
+                 lambda: layer.forward_fp8(x, W_r, None, (q["W1"][0], q["W1"][1][:, :1]), q["W3"], q["W2"]),
+                 lambda: layer.forward_fp8(x, W_r, None, q["W2"], q["W3"], q["W2"]),
+                 lambda: layer.forward_fp8(x, W_r, None, q["W1"], q["W3"], q["W2"], out=torch.empty_like(x).float())):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(MoEError):  # a SwiGLU layer without W3
+        layer.forward_fp8(x, W_r, None, q["W1"], None, q["W2"])
