@@ -852,17 +852,24 @@ int fp8_ksplit(int64_t rows, int G, int N, int K) {
   const int64_t tiles = (g + (rows - g) / BM) * ((N + 255) / 256);
   const int64_t num_kb = (K + BK - 1) / BK;
   if (tiles <= 0 || tiles > 4 * kSplitTargetCtas) return 1;
-  // Time of a cut, in tenths of a k-block's: the longest CTA runs ceil(units /
-  // SMs) ranges of `per` k-blocks, each followed by an epilogue (5 k-blocks for
-  // a full tile; next to nothing for a few rows, whose weight stream goes on
-  // under it); every partial is written and read once more (a k-block's time
-  // moves 2.7 MB), and a cut product needs a second launch (8 k-blocks of the
-  // tensor cores' time, 3.5 of the weight stream's).  Rows count in powers of
-  // two, so that the choice is constant between them.
+  // Rows count in powers of two, so that the choice is constant between them.
   int64_t r2 = 1;
   while (r2 < rows) r2 <<= 1;
-  const int64_t epi = r2 <= 64 ? 2 : 50;
-  const int64_t launch = r2 <= 64 ? 35 : 80;
+  if (r2 <= 64) {
+    // A few rows: the weights' stream is the time, and 48 CTAs with 160 KB in
+    // flight each carry most of what HBM gives (one token times 14336 x 4096: 56
+    // tiles uncut 20.1 us, cut in five 20.7 us with the second launch; the first
+    // projections of two experts of that size uncut 52 us, cut in three 57 us).
+    if (tiles >= 48) return 1;
+    const int64_t ks = std::min((96 + tiles - 1) / tiles, std::max<int64_t>(num_kb / 2, 1));
+    const int64_t per = (num_kb + ks - 1) / ks;
+    return static_cast<int>((num_kb + per - 1) / per);
+  }
+  // Time of a cut, in tenths of a k-block's: the longest CTA runs ceil(units /
+  // SMs) ranges of `per` k-blocks, each followed by an epilogue of about 5
+  // k-blocks' time; every partial is written and read once more (a k-block's
+  // time moves 2.7 MB), and a cut product needs a second launch (8).
+  const int64_t epi = 50, launch = 80;
   int64_t best = 1, best_t = (tiles + kSplitTargetCtas - 1) / kSplitTargetCtas * (10 * num_kb + epi);
   for (int64_t ks = 2; ks <= num_kb / 2; ++ks) {
     const int64_t per = (num_kb + ks - 1) / ks;
