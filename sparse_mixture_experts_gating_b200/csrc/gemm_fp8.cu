@@ -896,10 +896,11 @@ cudaError_t plan_fp8(const Fp8Args& g, Fp8Plan* pl, const char** why) {
   const uint32_t abox[2] = {static_cast<uint32_t>(BK), static_cast<uint32_t>(pl->ar)};
   const uint64_t K = g.K, N = g.N, G = g.G, ldb = g.ldb, gsb = g.gsb;
   if (!make_map_nd(&pl->a, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.A, 2, ad, as, abox) || !map_3d(&pl->b0, g.B0, K, N, G, ldb, gsb, pair ? 128 : 256) ||
-      !map_3d(&pl->b1, pair ? g.B1 : g.B0, K, N, G, ldb, gsb, 128)) {
+      (pair && !map_3d(&pl->b1, g.B1, K, N, G, ldb, gsb, 128))) {
     *why = "cuTensorMapEncodeTiled failed (alignment or driver entry point)";
     return cudaErrorInvalidValue;
   }
+  if (!pair) pl->b1 = pl->b0;  // (not read)
   Fp8Params& p = pl->p;
   p.G = g.G;
   p.N = g.N;

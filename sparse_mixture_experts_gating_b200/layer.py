@@ -44,11 +44,25 @@ def _switched(index: int, stream):
         yield torch._C._cuda_getCurrentRawStream(index)
 
 
+class _Here:
+    """The context of a call on the current device and its current stream."""
+    __slots__ = ("handle",)
+
+    def __init__(self, handle: int):
+        self.handle = handle
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *exc):
+        return False
+
+
 def _on(index: int, stream):
     """A context that runs on the tensors' device and on ``stream`` (None: that
     device's current stream) and yields the stream's handle."""
-    if stream is None and torch.cuda.current_device() == index:
-        return contextlib.nullcontext(torch._C._cuda_getCurrentRawStream(index))
+    if stream is None and torch._C._cuda_getDevice() == index:
+        return _Here(torch._C._cuda_getCurrentRawStream(index))
     return _switched(index, stream)
 
 
@@ -65,14 +79,16 @@ def _device_of(name, t) -> int:
 
 def _check_tensor(name, t, index, dtype, shape=None, contiguous=True):
     """A tensor on CUDA device ``index`` of the dtype, the shape and (by default) contiguous."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.get_device() == index
+            and (shape is None or t.shape == shape) and (not contiguous or t.is_contiguous())):
+        return
     if _device_of(name, t) != index:
         raise ValueError(f"{name}: want a tensor on cuda:{index}, got {t.device}")
     if t.dtype is not dtype:
         raise ValueError(f"{name}: want {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: want shape {tuple(shape)}, got {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name}: want a contiguous tensor")
+    raise ValueError(f"{name}: want a contiguous tensor")
 
 
 def _debug_struct(debug: Optional[dict], events, stream) -> Optional[MoEDebug]:
@@ -318,22 +334,24 @@ def quantize_int4(W: torch.Tensor, stream=None):
 def _rows_of(t: torch.Tensor):
     """(matrices, rows, columns, row stride) of a tensor read as matrices
     [rows][columns] laid out one after another, or None if it is not."""
-    if t.dim() < 2 or t.stride(-1) != 1 and t.shape[-1] > 1:
+    shape, strides = t.shape, t.stride()
+    n = len(shape)
+    if n < 2 or strides[-1] != 1 and shape[-1] > 1:
         return None
-    if t.dim() == 2:
-        (rows, cols), ld = t.shape, t.stride(0)
+    rows, cols, ld = shape[-2], shape[-1], strides[-2]
+    if n == 2:
         if rows <= 1:  # one row: its stride says nothing
             ld = (cols + 15) // 16 * 16
         return (1, rows, cols, ld) if ld >= cols else None
-    rows, cols = t.shape[-2:]
-    ld = t.stride(-2) if rows > 1 else max(t.stride(-2), cols)
+    if rows <= 1:
+        ld = max(ld, cols)
     if ld < cols:
         return None
     mats, step = 1, rows * ld
-    for n, s in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
-        if n != 1 and s != step:
+    for d in range(n - 3, -1, -1):
+        if shape[d] != 1 and strides[d] != step:
             return None
-        mats, step = mats * n, step * n
+        mats, step = mats * shape[d], step * shape[d]
     return mats, rows, cols, ld
 
 
@@ -345,7 +363,8 @@ def quantize_fp8(x: torch.Tensor, *, block_rows: int = 1, transpose: bool = Fals
     boundaries (a view of a wider tensor where the row length is no multiple
     of 16); scales are [..., ceil(rows / block_rows), ceil(columns / 128)]."""
     dev = _device_of("x", x)
-    if x.dim() < 2 or x.dtype not in DTYPE:
+    dtype = DTYPE.get(x.dtype)
+    if dtype is None or x.dim() < 2:
         raise ValueError(f"quantize_fp8: x is bf16 or fp32 with at least two dimensions, got {x.dtype} {tuple(x.shape)}")
     if block_rows != 1 and block_rows != 128:
         raise ValueError("quantize_fp8: block_rows must be 1 or 128")
@@ -357,12 +376,15 @@ def quantize_fp8(x: torch.Tensor, *, block_rows: int = 1, transpose: bool = Fals
         mats, R, K, ld = form
         rows, cols = (K, R) if transpose else (R, K)
         pitch = (cols + 15) // 16 * 16
-        lead = x.shape[:-2]
-        codes = x.new_empty(lead + (rows, pitch), dtype=FP8)
+        shape, scale_shape = (rows, pitch), ((rows + block_rows - 1) // block_rows, (cols + 127) // 128)
+        if x.dim() > 2:
+            lead = x.shape[:-2]
+            shape, scale_shape = lead + shape, lead + scale_shape
+        codes = x.new_empty(shape, dtype=FP8)
         if pitch != cols:
             codes = codes[..., :cols]
-        scales = x.new_empty(lead + ((rows + block_rows - 1) // block_rows, _blocks(cols)), dtype=torch.float32)
-        check(lib().moe_quantize_fp8(x.data_ptr(), DTYPE[x.dtype], mats, R, K, ld, block_rows, int(transpose),
+        scales = x.new_empty(scale_shape, dtype=torch.float32)
+        check(lib().moe_quantize_fp8(x.data_ptr(), dtype, mats, R, K, ld, block_rows, 1 if transpose else 0,
                                      codes.data_ptr(), pitch, scales.data_ptr(), handle))
     return codes, scales
 
@@ -375,21 +397,25 @@ def matmul_fp8(a, b, *, offsets: Optional[torch.Tensor] = None, out_dtype=torch.
     they were in ``out``.  Returns [M, N] in out_dtype (bf16 or fp32)."""
     (ac, sa), (bc, sb) = a, b
     dev = _device_of("a codes", ac)
+    out_kind = DTYPE.get(out_dtype)
+    if out_kind is None:
+        raise ValueError(f"matmul_fp8: out_dtype is bf16 or fp32, got {out_dtype}")
     _check_tensor("a codes", ac, dev, FP8, contiguous=False)
     _check_tensor("b codes", bc, dev, FP8, contiguous=False)
-    if ac.dim() != 2 or bc.dim() != (2 if offsets is None else 3) or ac.shape[1] != bc.shape[-1]:
+    sha, shb = ac.shape, bc.shape
+    if len(sha) != 2 or len(shb) != (2 if offsets is None else 3) or sha[1] != shb[-1]:
         raise ValueError(f"matmul_fp8: a [M, K] and b {'[N, K]' if offsets is None else '[G, N, K]'}, got "
-                         f"{tuple(ac.shape)} and {tuple(bc.shape)}")
-    M, K = ac.shape
-    N, lead, kb = bc.shape[-2], bc.shape[:-2], _blocks(K)
-    G = 1 if offsets is None else lead[0]
+                         f"{tuple(sha)} and {tuple(shb)}")
+    M, K = sha
+    N, kb, G = shb[-2], (K + 127) // 128, 1
     _check_tensor("a scales", sa, dev, torch.float32, (M, kb))
-    b_rows = 1 if sb.dim() == bc.dim() and sb.shape[-2] == N and N > 1 else 128
-    _check_tensor("b scales", sb, dev, torch.float32, lead + (N if b_rows == 1 else _blocks(N), kb))
+    b_rows = 1 if sb.dim() == len(shb) and sb.shape[-2] == N and N > 1 else 128
+    scale_shape = (N if b_rows == 1 else (N + 127) // 128, kb)
     if offsets is not None:
+        G = shb[0]
+        scale_shape = (G,) + scale_shape
         _check_tensor("offsets", offsets, dev, torch.int32, (G + 1,))
-    if out_dtype not in DTYPE:
-        raise ValueError(f"matmul_fp8: out_dtype is bf16 or fp32, got {out_dtype}")
+    _check_tensor("b scales", sb, dev, torch.float32, scale_shape)
     fa, fb = _rows_of(ac), _rows_of(bc)
     if fa is None or fb is None:
         raise ValueError("matmul_fp8: the codes' rows must be contiguous, their matrices one after another")
@@ -407,7 +433,8 @@ def matmul_fp8(a, b, *, offsets: Optional[torch.Tensor] = None, out_dtype=torch.
         n = L.moe_matmul_fp8_workspace_bytes(M, N, K, G)
         ws = sa.new_empty(n, dtype=torch.uint8) if n else None
         check(L.moe_matmul_fp8(M, N, K, G, ac.data_ptr(), fa[3], sa.data_ptr(), bc.data_ptr(), fb[3], sb.data_ptr(),
-                               b_rows, _ptr(offsets), out.data_ptr(), DTYPE[out_dtype], ld_out, _ptr(ws), n, handle))
+                               b_rows, None if offsets is None else offsets.data_ptr(), out.data_ptr(), out_kind, ld_out,
+                               None if ws is None else ws.data_ptr(), n, handle))
     return out
 
 
@@ -439,14 +466,15 @@ def router_balance(logits: torch.Tensor, k: int, *, offsets: Optional[torch.Tens
     scoring: "softmax" or "sigmoid" (normalised over the experts)."""
     dev, T, E, B = _balance_args("router_balance", logits, k, offsets, mask, scoring)
     with _on(dev, stream) as handle:
-        aux, z = logits.new_empty(B, dtype=torch.float32), logits.new_empty(B, dtype=torch.float32)
-        counts, tokens = logits.new_empty((B, E), dtype=torch.int32), logits.new_empty(B, dtype=torch.int32)
+        f32, i32, new = torch.float32, torch.int32, logits.new_empty
+        aux, z, counts, tokens = new(B, dtype=f32), new(B, dtype=f32), new((B, E), dtype=i32), new(B, dtype=i32)
         L = lib()
         n = L.moe_router_balance_workspace_bytes(T, E, B)
-        ws = logits.new_empty(n, dtype=torch.uint8)
+        ws = new(n, dtype=torch.uint8)
         check(L.moe_router_balance(T, E, k, logits.data_ptr(), DTYPE[logits.dtype], SCORING[scoring], B,
-                                   _ptr(offsets), _ptr(mask), aux.data_ptr(), z.data_ptr(), counts.data_ptr(),
-                                   tokens.data_ptr(), ws.data_ptr(), n, handle))
+                                   None if offsets is None else offsets.data_ptr(),
+                                   None if mask is None else mask.data_ptr(), aux.data_ptr(), z.data_ptr(),
+                                   counts.data_ptr(), tokens.data_ptr(), ws.data_ptr(), n, handle))
     return aux, z, counts, tokens
 
 
