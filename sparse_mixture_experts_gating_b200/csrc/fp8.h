@@ -90,8 +90,9 @@ struct Fp8Plan {
 };
 
 // K ranges of a product with at most `rows` rows over G groups, for one whose
-// output tiles alone cannot occupy the GPU.
-int fp8_ksplit(int64_t rows, int G, int N, int K);
+// output tiles alone cannot occupy the GPU.  summed_anyway: its partials cost no
+// launch of their own.
+int fp8_ksplit(int64_t rows, int G, int N, int K, bool summed_anyway = false);
 cudaError_t plan_fp8(const Fp8Args& g, Fp8Plan* plan, const char** why);
 cudaError_t launch_fp8(const Fp8Plan& plan, int num_sms, cudaStream_t s);
 

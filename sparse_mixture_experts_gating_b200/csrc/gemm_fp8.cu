@@ -846,7 +846,7 @@ cudaError_t launch_ar(const Fp8Plan& pl, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
-int fp8_ksplit(int64_t rows, int G, int N, int K) {
+int fp8_ksplit(int64_t rows, int G, int N, int K, bool summed_anyway) {
   // Most 128-row tiles `rows` rows can make over G groups.
   const int64_t g = std::min<int64_t>(G, rows);
   const int64_t tiles = (g + (rows - g) / BM) * ((N + 255) / 256);
@@ -856,12 +856,17 @@ int fp8_ksplit(int64_t rows, int G, int N, int K) {
   int64_t r2 = 1;
   while (r2 < rows) r2 <<= 1;
   if (r2 <= 64) {
-    // A few rows: the weights' stream is the time, and 48 CTAs with 160 KB in
-    // flight each carry most of what HBM gives (one token times 14336 x 4096: 56
-    // tiles uncut 20.1 us, cut in five 20.7 us with the second launch; the first
-    // projections of two experts of that size uncut 52 us, cut in three 57 us).
-    if (tiles >= 48) return 1;
-    const int64_t ks = std::min((96 + tiles - 1) / tiles, std::max<int64_t>(num_kb / 2, 1));
+    // A few rows: the weights' stream is the time, and about 96 CTAs carry what
+    // HBM gives (a k-block takes a CTA 0.45 us, 73 GB/s).  One token times 14336 x
+    // 4096, 56 tiles: uncut 19.8 us, cut in two 18.2 us, in five 20.7 us, each
+    // with the second launch; 224 tiles, two experts' first projections: uncut 52
+    // us, cut in three 57 us.
+    // Where a launch that follows sums the partials anyway, a cut is free, and
+    // fills the SMs (one token's second projections, 32 tiles: three ranges 30.0 us,
+    // four 29.4 us).
+    if (!summed_anyway && tiles >= 96) return 1;
+    const int64_t want = summed_anyway ? std::max<int64_t>(kSplitTargetCtas / tiles, 1) : (96 + tiles - 1) / tiles;
+    const int64_t ks = std::min(want, std::max<int64_t>(num_kb / 2, 1));
     const int64_t per = (num_kb + ks - 1) / ks;
     return static_cast<int>((num_kb + per - 1) / per);
   }

@@ -114,7 +114,7 @@ int w4_ksplit(int64_t s, int groups, int d, int d_ff) {
 
 int ksplit_of(const moe_layer& L, int64_t s_max, Weights kind) {
   if (kind == W_INT4) return w4_ksplit(s_max, L.E + L.n_shared, L.d, L.d_ff);
-  if (kind == W_FP8) return fp8_ksplit(s_max, L.E + L.n_shared, L.d, L.d_ff);
+  if (kind == W_FP8) return fp8_ksplit(s_max, L.E + L.n_shared, L.d, L.d_ff, true);
   return (L.dtype == MOE_BF16 && need_yp_of(L, kind)) ? gemm2_ksplit(s_max, L.E + L.n_shared, L.d, L.d_ff) : 1;
 }
 
