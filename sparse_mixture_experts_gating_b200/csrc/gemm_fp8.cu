@@ -6,22 +6,27 @@
 // for the rows r of every group g (offsets on the device; one group without
 // them).  The scales are arbitrary fp32 numbers, so the tensor core sums one
 // k-block of 128 (one 128-byte swizzled row of shared memory, four MMAs of
-// K = 32) into its own TMEM accumulator, and the epilogue warps read it back,
+// K = 32) into its own TMEM accumulator, and the summing warps read it back,
 // multiply by sa * sb and add it to fp32 registers while the next k-block's
-// MMAs fill the other accumulator.  Tiles are 128 rows x 256 columns: a
-// k-block's MMAs take 512 cycles at the tensor cores' rate, its read-back and
-// promotion 128 columns for each of the eight epilogue warps.
+// MMAs fill the other accumulator.  Tiles are 128 rows x 256 columns.
+//
+// What bounds it: a k-block's MMAs take 514 cycles, its 32768 additions 256 (the
+// fp32 rate of an SM) and its read-back 144, which add up to 320-400 in a loop
+// of nothing else; with the barriers, scales and moves between registers a
+// k-block takes about 900.  8192 x 14336 x 4096: 456 us in bursts (2.1
+// PFLOP/s), 507-520 us back to back, where the board's power limit sets the
+// clock (cuBLAS with one scale per tensor: 331 and 385 us).  Eight summing warps
+// of 128 columns with 232 registers each were the fastest of the forms tried;
+// sixteen of 64 columns, MMAs of half the width with four accumulators, and
+// sums kept in register pairs took 1.1 to 1.4 times as long.
 //
 // Warp roles (384 threads, one CTA per SM):
 //   warp 0       TMA producer
-//   warps 1, 2   lane 0 of each issues the tcgen05.mma of every other k-block:
-//                the issue of a k-block's MMAs returns when they are nearly
-//                done, so one thread alone would leave the tensor core idle
-//                while it waits for the next block's barriers (warp 1 also
-//                allocates TMEM)
-//   warp 3       none (it completes the warpgroup that gives its registers away)
-//   warps 4..11  promotion and epilogue: warp w owns TMEM lanes 32 (w % 4) ..
+//   warp 1       TMEM allocator; lane 0 issues tcgen05.mma
+//   warp 3       column scales (SB1)
+//   warps 4..11  summing and epilogue: warp w owns TMEM lanes 32 (w % 4) ..
 //                (rows of the tile) and the columns of half (w - 4) / 4
+//   (warps 0..3 are the warpgroup that gives its registers to the other two)
 // Pipelines: a ring of shared-memory stages (full / empty) and two TMEM
 // accumulators of 256 columns (tfull / tempty), one k-block each.  Every wait
 // is bounded; one that runs out records MOE_ERR_TIMEOUT, raises the CTA's
@@ -82,7 +87,7 @@ struct Ctl {
   uint64_t empty[MAX_STAGES];
   uint64_t tfull[2];
   uint64_t tempty[2];
-  uint64_t drain[2];
+  uint64_t drain;
   uint32_t tmem_slot;
   volatile int abort;
   int mprefix[kFp8MaxGroups + 1];
@@ -249,7 +254,7 @@ __device__ __forceinline__ void fma2(float& d0, float& d1, uint32_t a0, uint32_t
 
 // acc[i] += t[i] * (a scale): one scale for all 32 columns, or (SB1) one for each in `b`.
 template <bool SB1>
-__device__ __forceinline__ void promote32(float* acc, const uint32_t (&t)[32], float s, const float* b) {
+__device__ __forceinline__ void add32(float* acc, const uint32_t (&t)[32], float s, const float* b) {
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
     float s0 = s, s1 = s, s2 = s, s3 = s;
@@ -314,7 +319,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) { mbar_init(&ctl->full[s], 1); mbar_init(&ctl->empty[s], 1); }
     for (int a = 0; a < 2; ++a) { mbar_init(&ctl->tfull[a], 1); mbar_init(&ctl->tempty[a], EPI_WARPS); }
-    for (int a = 0; a < 2; ++a) mbar_init(&ctl->drain[a], 1);
+    mbar_init(&ctl->drain, 1);
     for (int s = 0; s < SB_SLOTS; ++s) { mbar_init(&ctl->sfull[s], 32); mbar_init(&ctl->sempty[s], EPI_WARPS); }
     ctl->abort = 0;
     fence_mbarrier_init();
@@ -362,43 +367,39 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int s = 0; s < STAGES; ++s)
         if ((issued >> s) & 1u) mbar_wait(&ctl->full[s], (issued_phase >> s) & 1u, p.limit_ns);
     }
-  } else if (warp <= 2) {
-    // ------------------------------------------------------------ MMA issuers
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      const int acc = warp - 1;  // this warp's accumulator: k-blocks acc, acc + 2, ... of the CTA's
-      int stage = 0, turn = 0;
+      int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * MMA_N);
       for (int64_t u = blockIdx.x; ok && item_at(ctl, p, u, w); u += gridDim.x) {
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (turn == acc) {
-            if (!mbar_wait_or_abort(&ctl->tempty[acc], acc_phase ^ 1u, &ctl->abort, p.err, p.limit_ns) ||
-                !mbar_wait_or_abort(&ctl->full[stage], phase, &ctl->abort, p.err, p.limit_ns)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t sa = smem_u32(stages + stage * STAGE_BYTES);
-#pragma unroll
-            for (int k = 0; k < BK / 32; ++k)
-              umma_f8(d_tmem, sdesc_k_sw128(sa + k * 32), sdesc_k_sw128(sa + A_ST + k * 32), IDESC, k != 0 ? 1u : 0u);
-            umma_commit(&ctl->empty[stage]);
-            umma_commit(&ctl->tfull[acc]);
-            acc_phase ^= 1u;
+          if (!mbar_wait_or_abort(&ctl->tempty[acc], acc_phase ^ 1u, &ctl->abort, p.err, p.limit_ns) ||
+              !mbar_wait_or_abort(&ctl->full[stage], phase, &ctl->abort, p.err, p.limit_ns)) {
+            ok = false;
+            break;
           }
-          turn ^= 1;
+          tc_fence_after();
+          const uint32_t sa = smem_u32(stages + stage * STAGE_BYTES);
+          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * MMA_N);
+#pragma unroll
+          for (int k = 0; k < BK / 32; ++k)
+            umma_f8(d_tmem, sdesc_k_sw128(sa + k * 32), sdesc_k_sw128(sa + A_ST + k * 32), IDESC, k != 0 ? 1u : 0u);
+          umma_commit(&ctl->empty[stage]);
+          umma_commit(&ctl->tfull[acc]);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
         }
       }
-      // Drain: all MMAs of this thread complete before TMEM is freed.
-      umma_commit(&ctl->drain[acc]);
-      mbar_wait(&ctl->drain[acc], 0, p.limit_ns);
+      // Drain: all MMAs of this CTA complete before TMEM is freed.
+      umma_commit(&ctl->drain);
+      mbar_wait(&ctl->drain, 0, p.limit_ns);
     }
-  } else if (SB1) {
+  } else if (SB1 && warp == 3) {
     // ------------------------------------------------------------ column scales
-    // (fetched by the summing threads themselves, a column each, one k-block's
-    // scales took two microseconds: a row of 65 scales shares no line with the next)
+    // Neighbouring columns' scales lie a row of B's scales apart, a cache line
+    // each: copied four k-blocks ahead, they keep that off the summing warps.
     int slot = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");
   }
   } else {
-    // ------------------------------------------------------------ promotion and epilogue
+    // ------------------------------------------------------------ summing and epilogue
     reg_inc<REGS_SUM>();
     const int q = warp & 3, half = (warp - 4) >> 2;
     const int r_in_tile = q * 32 + lane;
@@ -475,18 +476,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             tmem_ld32(tb + col0, t);
             tmem_ld_wait32(t);
             tmem_ld32(tb + col0 + 32, v);
-            promote32<SB1>(acc, t, s0, sbs);
+            add32<SB1>(acc, t, s0, sbs);
             tmem_ld_wait32(v);
             tmem_ld32(tb + col2, t);
-            promote32<SB1>(acc + 32, v, s0, sbs + 32);
+            add32<SB1>(acc + 32, v, s0, sbs + 32);
             tmem_ld_wait32(t);
             tmem_ld32(tb + col2 + 32, v);
-            promote32<SB1>(acc + 64, t, s1, sbs + 64);
+            add32<SB1>(acc + 64, t, s1, sbs + 64);
             tmem_ld_wait32(v);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->tempty[acc_i]);
-            promote32<SB1>(acc + 96, v, s1, sbs + 96);
+            add32<SB1>(acc + 96, v, s1, sbs + 96);
           } else {
             tc_fence_before();
             __syncwarp();
