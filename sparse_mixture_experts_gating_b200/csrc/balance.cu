@@ -194,9 +194,9 @@ __device__ __forceinline__ void choose_ordered(const float (&v)[J], int e0, int 
 
 // The same by the k-th largest: what reaches it is chosen.
 //
-// fp32: where exactly k values reach it they are the choices.  Ties at it, or
-// above it (heads taken off in step), leave more than k, and the warp then
-// chooses by definition.
+// fp32: where at most k values reach it they are the choices.  Ties at it, or
+// above it (heads taken off in step, until none may be left), leave more than
+// k, and the warp then chooses by definition.
 //
 // bf16 logits tie often, but fit the upper half of a 32-bit key whose lower
 // half holds the expert's place: no two keys are equal, and their order is the
@@ -224,7 +224,7 @@ __device__ __forceinline__ void choose(const float (&v)[J], int e0, int k, float
       mine += hit[j];
     }
     const float all = group_sum<W>(mine);
-    if (__any_sync(0xffffffffu, th > -INFINITY && all != static_cast<float>(k))) {
+    if (__any_sync(0xffffffffu, all > static_cast<float>(k))) {
       choose_ordered<W, J>(v, e0, k, cn);
     } else {
 #pragma unroll

@@ -114,6 +114,22 @@ def test_ties_go_to_the_lower_index():
     assert torch.equal(counts, expect) and tokens.item() == 40
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("E", [1, 2, 5, 8, 9, 16, 31, 64, 100, 256])
+@pytest.mark.parametrize("k", [1, 2, 4, 8])
+def test_rows_of_few_values(E, k, dtype):
+    """Logits all alike, or of two or three values, with some experts at -inf."""
+    if k > E:
+        pytest.skip("k <= E")
+    g = torch.Generator(device="cuda").manual_seed(E * 10 + k)
+    l = torch.randint(0, 3, (240, E), device="cuda", generator=g).float()
+    l[:80] = 0.0
+    l[40:80, ::2] = -0.0
+    l[80:160] = l[80:160].clamp(max=1)
+    l[torch.rand((240, E), device="cuda", generator=g) < torch.linspace(0, 0.9, 240, device="cuda")[:, None]] = float("-inf")
+    check(l.to(dtype), k, [0, 1, 40, 80, 160, 240], None, "softmax")
+
+
 def test_nothing_to_count():
     l, _ = make(10, 6, 3, F32, False, False)
     off = torch.tensor([0, 10], dtype=torch.int32, device="cuda")
