@@ -102,17 +102,23 @@ __device__ __forceinline__ float ex2(float v) {
 // softmax numerators ex and their sum over the row, of values v with row maximum
 // m: exp(v - m) as 2^(v log2 e - m log2 e), one fused operation and one of the
 // special function unit.  (The rounding of m log2 e is common to the row, so
-// it cancels in the scores.)
+// it cancels in the scores, and in m + log of the sum it is as small as m's
+// own.)  Beyond |m| = 2^16 that rounding could leave the exponential's range
+// (rows of a mask's huge value), and the difference is taken first.
 template <int W, int J>
 __device__ __forceinline__ float exp_sum(const float (&v)[J], float m, float (&ex)[J]) {
   constexpr float kLog2e = 1.4426950408889634f;
-  const float c = m * kLog2e;
   float s = 0.f;
+  if (fabsf(m) < 65536.f) {
+    const float c = m * kLog2e;
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    ex[j] = ex2(fmaf(v[j], kLog2e, -c));
-    s += ex[j];
+    for (int j = 0; j < J; ++j) ex[j] = ex2(fmaf(v[j], kLog2e, -c));
+  } else {
+#pragma unroll
+    for (int j = 0; j < J; ++j) ex[j] = ex2((v[j] - m) * kLog2e);
   }
+#pragma unroll
+  for (int j = 0; j < J; ++j) s += ex[j];
   return group_sum<W>(s);
 }
 

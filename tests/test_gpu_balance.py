@@ -105,6 +105,42 @@ def test_far_logits_neither_overflow_nor_vanish():
             assert np.abs(d.cpu().numpy() - rd).max() <= 1e-4 * scale
 
 
+@pytest.mark.parametrize("E", [5, 20, 64, 200])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_rows_of_the_lowest_value_and_other_far_ones(dtype, scoring, E):
+    """Experts masked by a huge finite value, all of a token's among them: their
+    scores are 0, or all alike."""
+    far = [torch.finfo(dtype).min, -1e30, -1e10, -1e9, 70000.0, 1e10, torch.finfo(dtype).max]
+    rows = []
+    for v in far:
+        whole = torch.full((E,), v)
+        one = whole.clone()
+        one[E // 2] = 1.0                                  # one other: the lowest lose to it, the largest win
+        two = torch.zeros(E)
+        two[[1, 3]] = v
+        rows += [whole, one, two]
+    l = torch.stack(rows).to(dtype).cuda().repeat_interleave(3, 0)   # a sequence of three tokens for each
+    B, k = len(rows), 2
+    cuts = [3 * b for b in range(B + 1)]
+    offsets = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+    daux = torch.linspace(-1, 2, B, device="cuda")
+    aux, z, counts, tokens, d = run(l, k, offsets, None, scoring, daux, None)
+    status()
+    lh = l.double().cpu().numpy()
+    ra, rz, rc, rt = D.loss(lh, k, cuts, None, scoring)
+    np.testing.assert_array_equal(counts.cpu().numpy(), rc)
+    np.testing.assert_array_equal(tokens.cpu().numpy(), rt)
+    # differences of two logits are 0, or far beyond the exponential's range, or (1 against 0) small
+    e = 80 * D.ULP
+    assert (np.abs(aux.cpu().numpy() - ra) <= e * np.abs(ra)).all()
+    with np.errstate(over="ignore"):
+        np.testing.assert_allclose(z.cpu().numpy(), rz.astype(np.float32), rtol=2 * e)  # (infinite beyond fp32)
+    rd, _ = D.gradient(lh, k, cuts, None, scoring, daux.double().cpu().numpy(), np.zeros(B))
+    bound = np.abs(daux.double().cpu().numpy()).repeat(3)[:, None] * E / 3  # |g| <= E |daux| / n, and so is its mean
+    assert (np.abs(d.cpu().numpy() - rd) <= 3 * e * 2 * bound * D.scores(lh, scoring) + 1e-37).all()
+
+
 def test_ties_go_to_the_lower_index():
     l = torch.zeros((40, 20), device="cuda")
     l[:, 7] = 1.0
