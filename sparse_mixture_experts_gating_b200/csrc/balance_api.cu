@@ -23,6 +23,9 @@ int done() {
   return MOE_OK;
 }
 
+// Tokens are counted in 31 bits, with room for a thread's steps past the last one.
+constexpr int64_t kMaxCount = 2147483647LL - 256;
+
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // The checks that both directions share; fills the common arguments.
@@ -35,7 +38,7 @@ int common(const std::string& F, int64_t T, int E, int k, const void* logits, in
   if (scoring != MOE_SCORE_SOFTMAX && scoring != MOE_SCORE_SIGMOID)
     return fail(MOE_ERR_INVALID_ARG, F + "unknown scoring");
   if (offsets == nullptr && sequences != 1) return fail(MOE_ERR_INVALID_ARG, F + "several sequences need their offsets");
-  if (T > 2147483647LL || sequences > 2147483647LL) return fail(MOE_ERR_UNSUPPORTED, F + "T or sequences too large");
+  if (T > kMaxCount || sequences > kMaxCount) return fail(MOE_ERR_UNSUPPORTED, F + "T or sequences too large");
   if (T > 0 && logits == nullptr) return fail(MOE_ERR_INVALID_ARG, F + "logits is NULL");
   if (!aligned(logits, dtype == MOE_BF16 ? 2 : 4) || !aligned(offsets, 4))
     return fail(MOE_ERR_INVALID_ARG, F + "logits and offsets must be aligned to their elements");
@@ -114,7 +117,8 @@ int router_balance_backward(int64_t T, int num_experts, int k, const void* logit
 extern "C" {
 
 size_t moe_router_balance_workspace_bytes(int64_t T, int num_experts, int64_t sequences) {
-  if (T < 0 || num_experts < 1 || num_experts > kBalanceMaxE || sequences < 0) return 0;
+  if (T < 0 || num_experts < 1 || num_experts > kBalanceMaxE || sequences < 0 || T > kMaxCount || sequences > kMaxCount)
+    return 0;
   return balance_workspace_bytes(T, num_experts, sequences);
 }
 

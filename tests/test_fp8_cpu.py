@@ -102,6 +102,13 @@ def test_balance_limits(L):
     assert L.moe_router_balance_workspace_bytes(0, 4, 3) >= 0
 
 
+@pytest.mark.parametrize("n", [(1 << 31) - 255, (1 << 31) - 1, 1 << 31, 1 << 60])
+def test_balance_counts_that_no_31_bit_step_passes(L, n):
+    assert balance(L, T=n) == UNSUPPORTED and backward(L, T=n) == UNSUPPORTED
+    assert balance(L, B=n, off=P) == UNSUPPORTED and backward(L, B=n, off=P) == UNSUPPORTED
+    assert L.moe_router_balance_workspace_bytes(n, 4, 1) == 0 and L.moe_router_balance_workspace_bytes(8, 4, n) == 0
+
+
 def create(L, *args):
     h = ctypes.c_void_p()
     assert L.moe_create(*args, ctypes.byref(h)) == 0
