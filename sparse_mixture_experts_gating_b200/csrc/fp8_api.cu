@@ -31,6 +31,12 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Floats between the rows of a partial: whole 16-byte pieces.
 int64_t partial_ld(int64_t N) { return (N + 3) / 4 * 4; }
 
+// Sizes whose rows, tiles and k-blocks the product counts in 31 bits.
+bool product_too_large(int64_t M, int64_t N, int64_t K, int64_t groups) {
+  return M > 2147483647LL - 256 || N > (int64_t{1} << 24) || K > (int64_t{1} << 30) ||
+         (M / 128 + groups) * ceil_div(N, 128) > 2147483647LL;
+}
+
 int quantize_fp8(const void* x, int dtype, int64_t matrices, int64_t rows, int64_t K, int64_t ld, int block_rows,
                      int transpose, void* codes, int64_t ld_codes, float* scales, void* stream) {
   const std::string F = "moe_quantize_fp8: ";
@@ -82,10 +88,10 @@ int matmul_fp8(int64_t M, int64_t N, int64_t K, int64_t groups, const void* a_co
   if (out_dtype != MOE_F32 && out_dtype != MOE_BF16) return fail(MOE_ERR_INVALID_ARG, F + "unknown out_dtype");
   if (b_rows != 1 && b_rows != F8_GROUP) return fail(MOE_ERR_INVALID_ARG, F + "b_rows must be 1 or 128");
   if (M == 0) return done();
-  if (M > 2147483647LL - 256 || N > (int64_t{1} << 24) || K > (int64_t{1} << 30) || lda >= (int64_t{1} << 40) ||
-      ldb >= (int64_t{1} << 40) || ldb > ((int64_t{1} << 40) - 1) / N)
-    return fail(MOE_ERR_UNSUPPORTED, F + "a size is too large");
-  if ((M / 128 + groups) * ceil_div(N, 128) > 2147483647LL) return fail(MOE_ERR_UNSUPPORTED, F + "too many output tiles");
+  if (product_too_large(M, N, K, groups)) return fail(MOE_ERR_UNSUPPORTED, F + "a size is too large");
+  if (lda >= (int64_t{1} << 40) || ldb >= (int64_t{1} << 40) || ldb > ((int64_t{1} << 40) - 1) / N ||
+      ld_out > (int64_t{1} << 60) / M)
+    return fail(MOE_ERR_UNSUPPORTED, F + "a row stride is too large");
   if (lda < K || ldb < K || ld_out < N) return fail(MOE_ERR_INVALID_ARG, F + "a row stride is smaller than its row");
   if (a_codes == nullptr || a_scales == nullptr || b_codes == nullptr || b_scales == nullptr || out == nullptr)
     return fail(MOE_ERR_INVALID_ARG, F + "NULL pointer");
@@ -164,8 +170,7 @@ int moe_quantize_fp8(const void* x, int dtype, int64_t matrices, int64_t rows, i
 }
 
 size_t moe_matmul_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t groups) {
-  if (M <= 0 || N <= 0 || K <= 0 || groups <= 0 || groups > kFp8MaxGroups || N > 2147483647LL || K > 2147483647LL)
-    return 0;
+  if (M <= 0 || N <= 0 || K <= 0 || groups <= 0 || groups > kFp8MaxGroups || product_too_large(M, N, K, groups)) return 0;
   const int ks = fp8_ksplit(M, static_cast<int>(groups), static_cast<int>(N), static_cast<int>(K));
   return ks > 1 ? sizeof(float) * static_cast<size_t>(ks) * static_cast<size_t>(M) * static_cast<size_t>(partial_ld(N)) : 0;
 }

@@ -877,7 +877,9 @@ int fp8_ksplit(int64_t rows, int G, int N, int K, bool summed_anyway) {
   // time moves 2.7 MB), and a cut product needs a second launch (8).
   const int64_t epi = 50, launch = 80;
   int64_t best = 1, best_t = (tiles + kSplitTargetCtas - 1) / kSplitTargetCtas * (10 * num_kb + epi);
-  for (int64_t ks = 2; ks <= num_kb / 2; ++ks) {
+  // (More ranges than two waves of CTAs, or sixteen of many tiles, gain under a tenth in this sum.)
+  const int64_t most = std::min<int64_t>(num_kb / 2, std::max<int64_t>(16, 2 * kSplitTargetCtas / tiles));
+  for (int64_t ks = 2; ks <= most; ++ks) {
     const int64_t per = (num_kb + ks - 1) / ks;
     const int64_t ranges = (num_kb + per - 1) / per;
     const int64_t t = (tiles * ranges + kSplitTargetCtas - 1) / kSplitTargetCtas * (10 * per + epi) +

@@ -69,6 +69,18 @@ def test_product_limits(L):
     assert L.moe_matmul_fp8_workspace_bytes(1, 256, 1 << 14, 1) >= 4 * 256  # one tile: K is cut
 
 
+def test_product_sizes_near_the_limits(L):
+    """No size overflows the plan: it is refused, and needs no workspace, or it is planned."""
+    for M, N, K, G in ((1 << 62, 1, 1, 1), (1, (1 << 31) - 1, 1, 1), (1, 1, (1 << 31) - 1, 1), ((1 << 31) - 1, 1, 1, 1),
+                       (1 << 30, 1 << 20, 64, 1)):
+        assert L.moe_matmul_fp8_workspace_bytes(M, N, K, G) == 0
+        assert mm(L, M=M, N=N, K=K, G=G, lda=1 << 31, ldb=1 << 31, ldo=1 << 31, off=P) == UNSUPPORTED
+    assert mm(L, ldo=1 << 60) == UNSUPPORTED and mm(L, ldb=1 << 39) == UNSUPPORTED
+    # 2^23 k-blocks: at most two waves of ranges are looked at, each with its partial
+    n = L.moe_matmul_fp8_workspace_bytes(128, 128, 1 << 30, 1)
+    assert 0 < n <= 2 * 148 * 128 * 128 * 4
+
+
 def balance(L, T=8, E=4, k=2, l=P, dt=0, sc=0, B=1, off=None, mask=None, aux=P, z=P, c=P, t=P, ws=P, n=1 << 40):
     return L.moe_router_balance(T, E, k, l, dt, sc, B, off, mask, aux, z, c, t, ws, n, None)
 
