@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 from typing import Optional
 
 import torch
@@ -343,8 +344,10 @@ def _rows_of(t: torch.Tensor):
         if rows <= 1:  # one row: its stride says nothing
             ld = (cols + 15) // 16 * 16
         return (1, rows, cols, ld) if ld >= cols else None
-    if rows <= 1:
-        ld = max(ld, cols)
+    if t.numel() == 0:
+        return math.prod(shape[:-2]), rows, cols, cols
+    if rows == 1:  # the matrices' stride is the row's
+        ld = next((strides[d] for d in range(n - 3, -1, -1) if shape[d] != 1), (cols + 15) // 16 * 16)
     if ld < cols:
         return None
     mats, step = 1, rows * ld

@@ -174,6 +174,27 @@ def test_binding_refuses_what_is_not_on_a_gpu():
             call()
 
 
+def test_rows_of_reads_every_contiguous_tensor():
+    """(matrices, rows, columns, row stride), whatever strides torch keeps for dimensions of one or none."""
+    from sparse_mixture_experts_gating_b200.layer import _rows_of
+    base = torch.zeros(1 << 16)
+    assert _rows_of(base.as_strided((4, 1, 8), (8, 100, 1))) == (4, 1, 8, 8)
+    assert _rows_of(base.as_strided((4, 1, 8), (16, 8, 1))) == (4, 1, 8, 16)   # one row of each pitch
+    assert _rows_of(base.as_strided((1, 1, 8), (3, 5, 1))) == (1, 1, 8, 16)
+    assert _rows_of(base.as_strided((2, 3, 1, 8), (24, 8, 999, 1))) == (6, 1, 8, 8)
+    assert _rows_of(base.as_strided((2, 5, 8), (80, 16, 1))) == (2, 5, 8, 16)
+    assert _rows_of(base.as_strided((2, 5, 8), (100, 16, 1))) is None           # a gap between matrices
+    assert _rows_of(base.as_strided((5, 8), (0, 1))) is None                    # one row, five times
+    assert _rows_of(base.as_strided((4, 1, 8), (0, 8, 1))) is None
+    assert _rows_of(base.as_strided((5, 8), (8, 2))) is None
+    for shape in ((2, 0, 8), (2, 5, 0), (0, 5, 8), (2, 3, 0, 8), (1, 1, 1), (3, 1, 1), (2, 1, 7), (1, 0, 8)):
+        t = torch.empty(shape)
+        mats, rows, cols, ld = _rows_of(t)
+        assert (mats * rows * cols, rows, cols) == (t.numel(), shape[-2], shape[-1]) and ld >= cols
+    for shape in ((0, 8), (1, 8), (3, 0), (1, 1)):
+        assert _rows_of(torch.empty(shape))[:3] == (1,) + shape
+
+
 # ------------------------------------------------------------------ the definitions the GPU tests use
 def test_e4m3_rounding_is_the_formats():
     """The table and the rounding of tests/_fp8.py against torch's conversion, over

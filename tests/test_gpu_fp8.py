@@ -74,6 +74,19 @@ def test_quantiser_reads_views_and_stacks():
     assert codes.shape == (0, 64) and scales.shape == (0, 1)
 
 
+def test_quantiser_takes_contiguous_tensors_of_any_stride():
+    base = torch.randn(4096, device="cuda", generator=gen(12))
+    for size, stride in (((4, 1, 200), (200, 999, 1)), ((4, 1, 200), (208, 200, 1)), ((2, 3, 1, 8), (24, 8, 77, 1)), ((3, 1, 1), (1, 5, 7))):
+        x = base.as_strided(size, stride)
+        for kw in (dict(), dict(block_rows=128), dict(transpose=True), dict(block_rows=128, transpose=True)):
+            codes, scales = quantize_fp8(x, **kw)
+            check_quantized(x, codes, scales, kw.get("block_rows", 1), kw.get("transpose", False))
+    for size in ((2, 0, 8), (2, 5, 0), (0, 5, 8)):
+        for tr in (False, True):
+            codes, scales = quantize_fp8(torch.empty(size, device="cuda"), transpose=tr)
+            assert codes.shape == (size if not tr else (size[0], size[2], size[1])) and scales.shape[0] == size[0]
+
+
 def test_quantiser_marks_what_is_not_finite():
     x = torch.randn((4, 256), device="cuda", generator=gen(3))
     x[1, 3] = float("nan")
@@ -141,6 +154,35 @@ def test_grouped_product(M, N, K, cuts, out_dtype):
             check_product(out[lo:hi], av[lo:hi], host((b[0][g], b[1][g]), 128), out_dtype)
     outside = torch.cat([out[: cuts[0]], out[cuts[-1]:]])
     assert (outside == 7.0).all()
+
+
+@pytest.mark.parametrize("b_rows", [128, 1])
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+@pytest.mark.parametrize("M,N,K", [(2100, 5000, 200), (1900, 5003, 300)])
+def test_more_tiles_than_sms(M, N, K, out_dtype, b_rows):
+    """Every CTA makes several tiles, whole and partial ones, with aligned rows and without."""
+    a, b = operands(M, N, K, None, b_rows, M)
+    y = matmul_fp8(a, b, out_dtype=out_dtype)
+    status()
+    check_product(y, host(a, 1), host(b, b_rows), out_dtype)
+
+
+@pytest.mark.parametrize("b_rows", [128, 1])
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+@pytest.mark.parametrize("M,N,K,G", [(20, 300, 5000, 3), (150, 260, 9000, 4), (2000, 1030, 260, 40), (40, 500, 130, 256)])
+def test_grouped_product_of_long_rows_and_many_groups(M, N, K, G, out_dtype, b_rows):
+    """K cut over the CTAs, and groups of every size, with either scale form of b."""
+    a, b = operands(M, N, K, G, b_rows, M + G)
+    cuts = np.sort(np.random.default_rng(G).integers(0, M + 1, G + 1))
+    out = torch.full((M, N), 7.0, dtype=out_dtype, device="cuda")
+    matmul_fp8(a, b, offsets=torch.from_numpy(cuts.astype(np.int32)).cuda(), out_dtype=out_dtype, out=out)
+    status()
+    av, bc, bs = host(a, 1), code_values(b[0]), b[1].cpu().numpy()
+    for g in range(G):
+        lo, hi = cuts[g], cuts[g + 1]
+        if hi > lo:
+            check_product(out[lo:hi], av[lo:hi], F.values(bc[g], bs[g], b_rows), out_dtype)
+    assert (out[:cuts[0]] == 7).all() and (out[cuts[-1]:] == 7).all()
 
 
 def test_product_writes_its_columns_only():
