@@ -268,12 +268,12 @@ __device__ __forceinline__ void add32(float* acc, const uint32_t (&t)[32], float
 }
 
 // silu(a) * b from the special function unit's exponential and reciprocal (each
-// good to two units; 0 once e^-a overflows, the limit of silu).
+// good to two units; 0 once e^-a overflows, the limit of silu, whatever a b is).
 __device__ __forceinline__ float silu_mul(float a, float b) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a * -1.4426950408889634f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  return a * b * r;
+  return a * r * b;
 }
 
 // 16 bytes of an output row: eight bf16, eight fp16 scaled by g, or four fp32 times g.

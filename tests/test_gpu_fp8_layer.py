@@ -171,6 +171,21 @@ def test_layer_is_its_operators_in_a_row():
     assert (np.abs(g["y_f32"] - y.cpu().numpy()) <= 2 * tol).all()
 
 
+@pytest.mark.parametrize("T", [3, 50, 200])
+def test_a_closed_gate_of_far_values_is_zero(T):
+    """silu(a) b where a is far below zero and a b past fp32's range: 0, not NaN."""
+    w = Workload("far_gate", T=T, d=256, E=2, k=1, d_ff=384, act=S, gate=SW, capacity_factor=0.0, dtype=DTYPE_BF16,
+                 dyadic=True, seed=52)
+    inp = make_inputs(w, device="cuda")
+    inp["x"].fill_(1.0)
+    inp["W1"].fill_(-2.0 ** 60)
+    inp["W3"].fill_(2.0 ** 60)
+    q = quantized(inp)
+    y, *_ = layer_for(w).forward_fp8(inp["x"], inp["W_r"], inp["b_r"], q["W1"], q["W3"], q["W2"])
+    status()
+    assert not y.any()
+
+
 def test_same_inputs_give_the_same_bits_and_calls_share_nothing():
     w = CASES[4]
     inp = make_inputs(w, device="cuda")
