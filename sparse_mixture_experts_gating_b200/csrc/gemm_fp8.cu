@@ -58,7 +58,9 @@ constexpr int NUM_THREADS = 384;
 constexpr int REGS_START = 168, REGS_FEED = 40, REGS_SUM = 232;
 static_assert(REGS_FEED + 2 * REGS_SUM <= 3 * REGS_START, "the registers of the launch");
 constexpr int EPI_WARPS = 8;
-constexpr int SB_SLOTS = 4;              // k-blocks of column scales in flight (SB1)
+// Column scales (SB1): a ring of SB_ROWS k-blocks, copied SB_KB at a time, in rows of
+// SB_LD floats, a bank apart by 8 so that 8 columns x 4 k-blocks take all 32.
+constexpr int SB_ROWS = 12, SB_KB = 4, SB_LD = MMA_N + 8;
 constexpr uint32_t TMEM_COLS = 2 * MMA_N;
 constexpr int ROW_STAGE = 64;           // bytes per staged output row of a warp's own stores
 constexpr int OUT_HALF = 2 * 16384;     // two boxes of 128 rows x 128 bytes of a warpgroup's TMA stores
@@ -93,19 +95,18 @@ struct Ctl {
   int mprefix[kFp8MaxGroups + 1];
   int offsets[kFp8MaxGroups + 1];
   float hmax[2][BM];
-  // per-row scales of B (SB1): a ring of k-blocks' 256 columns
-  uint64_t sfull[SB_SLOTS];
-  uint64_t sempty[SB_SLOTS];
-  alignas(16) float sb[SB_SLOTS][MMA_N];
 };
 
 // Byte offset of 16-byte piece v of staged row r: the pieces are permuted so that
 // eight rows written at one v, and two rows read at four, take all 32 banks.
 __device__ __forceinline__ int stage_at(int r, int v) { return r * ROW_STAGE + ((v ^ (r >> 1 & 3)) << 4); }
 
-template <int AR>
+constexpr size_t CTL_BYTES = (sizeof(Ctl) + 15) / 16 * 16;
+
+template <int AR, bool SB1>
 constexpr size_t smem_bytes() {
-  return Geo<AR>::STAGES * Geo<AR>::STAGE_BYTES + Geo<AR>::OUT_BYTES + sizeof(Ctl) + 1024;
+  return Geo<AR>::STAGES * Geo<AR>::STAGE_BYTES + Geo<AR>::OUT_BYTES + CTL_BYTES +
+         (SB1 ? sizeof(float) * SB_ROWS * SB_LD : 0) + 1024;
 }
 
 // kind::f8f6f4: e4m3 A and B (format fields 0, both K-major), fp32 D.
@@ -252,18 +253,33 @@ __device__ __forceinline__ void fma2(float& d0, float& d1, uint32_t a0, uint32_t
       : "r"(a0), "r"(a1), "f"(b0), "f"(b1));
 }
 
-// acc[i] += t[i] * (a scale): one scale for all 32 columns, or (SB1) one for each in `b`.
+// d = a * (b * s) + d on two fp32 numbers at once.
+__device__ __forceinline__ void mul_fma2(float& d0, float& d1, uint32_t a0, uint32_t a1, float b0, float b1, float s) {
+  asm("{\n\t.reg .b64 x, y, z, q;\n\t"
+      "mov.b64 q, {%6, %6};\n\t"
+      "mov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 y, y, q;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 z, {%0, %1};\n\t"
+      "fma.rn.f32x2 z, x, y, z;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}\n"
+      : "+f"(d0), "+f"(d1)
+      : "r"(a0), "r"(a1), "f"(b0), "f"(b1), "f"(s));
+}
+
+// acc[i] += t[i] * (a scale): one scale for all 32 columns, or (SB1) s times one for each in `b`.
 template <bool SB1>
 __device__ __forceinline__ void add32(float* acc, const uint32_t (&t)[32], float s, const float* b) {
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
-    float s0 = s, s1 = s, s2 = s, s3 = s;
     if (SB1) {
       const float4 v = *reinterpret_cast<const float4*>(b + i);
-      s0 *= v.x; s1 *= v.y; s2 *= v.z; s3 *= v.w;
+      mul_fma2(acc[i], acc[i + 1], t[i], t[i + 1], v.x, v.y, s);
+      mul_fma2(acc[i + 2], acc[i + 3], t[i + 2], t[i + 3], v.z, v.w, s);
+    } else {
+      fma2(acc[i], acc[i + 1], t[i], t[i + 1], s, s);
+      fma2(acc[i + 2], acc[i + 3], t[i + 2], t[i + 3], s, s);
     }
-    fma2(acc[i], acc[i + 1], t[i], t[i + 1], s0, s1);
-    fma2(acc[i + 2], acc[i + 3], t[i + 2], t[i + 3], s2, s3);
   }
 }
 
@@ -314,13 +330,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint8_t* stages = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* out_stage = stages + STAGES * STAGE_BYTES;
   Ctl* ctl = reinterpret_cast<Ctl*>(out_stage + G::OUT_BYTES);
+  float* sb_ring = reinterpret_cast<float*>(out_stage + G::OUT_BYTES + CTL_BYTES);  // SB1
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) { mbar_init(&ctl->full[s], 1); mbar_init(&ctl->empty[s], 1); }
+    for (int s = 0; s < STAGES; ++s) { mbar_init(&ctl->full[s], SB1 ? 33 : 1); mbar_init(&ctl->empty[s], 1); }
     for (int a = 0; a < 2; ++a) { mbar_init(&ctl->tfull[a], 1); mbar_init(&ctl->tempty[a], EPI_WARPS); }
     mbar_init(&ctl->drain, 1);
-    for (int s = 0; s < SB_SLOTS; ++s) { mbar_init(&ctl->sfull[s], 32); mbar_init(&ctl->sempty[s], EPI_WARPS); }
     ctl->abort = 0;
     fence_mbarrier_init();
     tma_prefetch_desc(&tmA);
@@ -398,24 +414,40 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
   } else if (SB1 && warp == 3) {
     // ------------------------------------------------------------ column scales
-    // Neighbouring columns' scales lie a row of B's scales apart, a cache line
-    // each: copied four k-blocks ahead, they keep that off the summing warps.
-    int slot = 0;
+    // Neighbouring columns' scales lie a row of B's scales apart.  A lane copies
+    // one k-block of a column, four lanes the chunk's, so that a request takes 8
+    // cache lines and a sector's neighbours are taken with it (k-block by k-block
+    // for 32 columns, 32 lines each, 4736 x 4096 x 4096 took 140 us).
+    //
+    // They need no barriers of their own (which cost every summing warp a wait and
+    // an arrival: 128 us against 115): a k-block's stage is full once its scales have landed
+    // too, so its MMAs' commit stands for both.  And k-block n is copied for after
+    // its stage came free, which is after the MMAs of k-block n - STAGES, which
+    // waited for the accumulator that the summing warps left before k-block n -
+    // STAGES - 1: their scales up to n - STAGES - 3 have been read.
+    static_assert(SB_KB - 1 - SB_ROWS <= -STAGES - 3 && SB_ROWS % SB_KB == 0, "the last row that a copy takes over has been read");
+    const int kl = lane & (SB_KB - 1), cl = lane >> 2;
+    int stage = 0, row = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int64_t u = blockIdx.x; ok && item_at(ctl, p, u, w); u += gridDim.x) {
-      const int col = w.nt * 256 + lane;
-      const float* sb = p.sb0 + w.g * p.sb_gs + static_cast<int64_t>(col) * p.num_kb;
+      const int col = w.nt * 256 + cl;
+      const float* sb = p.sb0 + w.g * p.sb_gs + static_cast<int64_t>(col) * p.num_kb + kl;
       for (int kb = w.kb0; kb < w.kb1; ++kb) {
         ok = __all_sync(0xffffffffu,
-                        mbar_wait_or_abort(&ctl->sempty[slot], phase ^ 1u, &ctl->abort, p.err, p.limit_ns));
+                        mbar_wait_or_abort(&ctl->empty[stage], phase ^ 1u, &ctl->abort, p.err, p.limit_ns));
         if (!ok) break;
-#pragma unroll
-        for (int i = 0; i < MMA_N / 32; ++i)
-          if (col + 32 * i < p.N)
-            cp_async4(&ctl->sb[slot][lane + 32 * i], sb + static_cast<int64_t>(32 * i) * p.num_kb + kb);
-        cp_async_arrive(&ctl->sfull[slot]);
-        if (++slot == SB_SLOTS) { slot = 0; phase ^= 1u; }
+        if (((kb - w.kb0) & (SB_KB - 1)) == 0 && kb + kl < w.kb1) {
+          int to = row + kl;
+          if (to >= SB_ROWS) to -= SB_ROWS;
+          float* dst = sb_ring + to * SB_LD + cl;
+#pragma unroll 8
+          for (int i = 0; i < MMA_N; i += 8)
+            if (col + i < p.N) cp_async4(dst + i, sb + static_cast<int64_t>(i) * p.num_kb + kb);
+        }
+        cp_async_arrive(&ctl->full[stage]);
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        if (++row == SB_ROWS) row = 0;
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -431,8 +463,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // PAIR: columns [64 half, +64) of W1, then of W3; else columns [128 half, +128)
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t col0 = PAIR ? 64u * half : 128u * half, col2 = PAIR ? 128u + 64u * half : 128u * half + 64u;
-    int acc_i = 0, slot = 0;
-    uint32_t acc_phase = 0, slot_phase = 0;
+    int acc_i = 0, sb_row = 0;
+    uint32_t acc_phase = 0;
     bool ok = true;
     for (int64_t u = blockIdx.x; ok && item_at(ctl, p, u, w); u += gridDim.x) {
       const int m_local = w.mt * BM + r_in_tile;
@@ -461,10 +493,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         a1 = scale_a(kb + 2);
         b1 = scale_b0(kb + 2);
         c1 = scale_b1(kb + 2);
-        const float* sbs = ctl->sb[slot] + half * 128;
-        if (SB1)
-          ok = ok && __all_sync(0xffffffffu,
-                                mbar_wait_or_abort(&ctl->sfull[slot], slot_phase, &ctl->abort, p.err, p.limit_ns));
+        const float* sbs = sb_ring + sb_row * SB_LD + half * 128;
         ok = ok && __all_sync(0xffffffffu,
                               mbar_wait_or_abort(&ctl->tfull[acc_i], acc_phase, &ctl->abort, p.err, p.limit_ns));
         if (ok) {
@@ -494,11 +523,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (lane == 0) mbar_arrive(&ctl->tempty[acc_i]);
           }
         }
-        if (SB1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->sempty[slot]);
-          if (++slot == SB_SLOTS) { slot = 0; slot_phase ^= 1u; }
-        }
+        if (SB1 && ++sb_row == SB_ROWS) sb_row = 0;
         if (++acc_i == 2) { acc_i = 0; acc_phase ^= 1u; }
         if (!ok) break;
       }
@@ -828,7 +853,7 @@ bool map_3d(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint64_
 
 template <int EPI, int AR, bool SB1>
 cudaError_t launch_t(const Fp8Plan& pl, int num_sms, cudaStream_t s) {
-  constexpr size_t bytes = smem_bytes<AR>();
+  constexpr size_t bytes = smem_bytes<AR, SB1>();
   static_assert(bytes <= 227 * 1024, "8-bit product: shared memory");
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(&fp8_gemm_kernel<EPI, AR, SB1>),
                                       static_cast<int>(bytes));
