@@ -609,6 +609,7 @@ int forward_impl(moe_handle h, int64_t T, const void* x, const float* W_r, const
   r.x = x;
   r.x_rows = fp8 ? static_cast<const void*>(ws + w.Xq) : x;
   r.d_rows = fp8 ? static_cast<int>(fp8_x_pitch(L) / 2) : L.d;
+  r.after_own = fp8;
   r.W_r = W_r;
   r.b_r = b_r;
   r.logits_in = dbg ? dbg->logits_in : nullptr;

@@ -113,6 +113,8 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const QuantFp8Args a, u
                                                          int step_groups, int vec_in, int vec_out) {
   static_assert(UNROLL == 4, "a lane divides for one group in four");
   const int l = threadIdx.x & 15;
+  pdl_wait();
+  pdl_trigger();
   // this team's first group; the next ones lie 16 groups = step_rows rows and step_groups groups on
   const uint32_t i0 = blockIdx.x * (16u * UNROLL) + (threadIdx.x >> 4);
   uint32_t r = i0 / static_cast<uint32_t>(kb_n);
@@ -173,6 +175,8 @@ __global__ void __launch_bounds__(256) quant_tile_kernel(const QuantFp8Args a, i
   __shared__ alignas(16) uint8_t s_t[TR ? 128 * 128 : 16];
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, warp = threadIdx.x >> 5;
   const uint32_t per = static_cast<uint32_t>(rb_n) * static_cast<uint32_t>(kb_n);
+  pdl_wait();
+  pdl_trigger();
   const uint32_t mat = blockIdx.x / per, tile = blockIdx.x - mat * per;
   const int rb = static_cast<int>(tile / static_cast<uint32_t>(kb_n));
   const int kb = static_cast<int>(tile - static_cast<uint32_t>(rb) * static_cast<uint32_t>(kb_n));
@@ -265,19 +269,13 @@ cudaError_t launch_x(const QuantFp8Args& a, cudaStream_t s) {
     // (matrices lie one after another, so their rows are rows of one)
     const int64_t rows = static_cast<int64_t>(a.G) * a.R, items = rows * kb;  // below 2^31
     const int64_t blocks = (items + 16 * UNROLL - 1) / (16 * UNROLL);
-    quant_rows_kernel<XT><<<static_cast<unsigned>(blocks), 256, 0, s>>>(a, static_cast<uint32_t>(rows), kb, 16 / kb,
-                                                                       16 % kb, vec_in, vec_out);
-  } else {
-    const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.G) * rb * kb);
-    if (a.block_rows == 128) {
-      if (a.transpose) quant_tile_kernel<XT, true, true><<<blocks, 256, 0, s>>>(a, rb, kb, vec_in, vec_out);
-      else quant_tile_kernel<XT, true, false><<<blocks, 256, 0, s>>>(a, rb, kb, vec_in, vec_out);
-    } else {
-      quant_tile_kernel<XT, false, true><<<blocks, 256, 0, s>>>(a, rb, kb, vec_in, vec_out);
-    }
+    return launch_pdl(quant_rows_kernel<XT>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a,
+                      static_cast<uint32_t>(rows), kb, 16 / kb, 16 % kb, vec_in, vec_out);
   }
-  count_launch();
-  return cudaGetLastError();
+  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.G) * rb * kb)), block(256);
+  if (a.block_rows != 128) return launch_pdl(quant_tile_kernel<XT, false, true>, grid, block, 0, s, a, rb, kb, vec_in, vec_out);
+  return a.transpose ? launch_pdl(quant_tile_kernel<XT, true, true>, grid, block, 0, s, a, rb, kb, vec_in, vec_out)
+                     : launch_pdl(quant_tile_kernel<XT, true, false>, grid, block, 0, s, a, rb, kb, vec_in, vec_out);
 }
 
 }  // namespace

@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(256) split_router_kernel(const float* __restri
     planes[n + i] = w1;
     planes[2 * n + i] = __float2bfloat16_rn(r2);
   }
+  pdl_wait();  // (RoutingArgs::after_own: what waits for this grid waits for the one before too)
 }
 
 // K (= top-k) is a template parameter so the running k-best list is indexed
@@ -632,10 +633,16 @@ cudaError_t launch_ep(const RoutingArgs& a, void* wsplit, void* partials, int nu
 
   const int64_t n = static_cast<int64_t>(EP) * a.d;
   const int sblocks = static_cast<int>((n + 255) / 256 < 4 * num_sms ? (n + 255) / 256 : 4 * num_sms);
-  split_router_kernel<<<sblocks, 256, 0, s>>>(a.W_r, a.E, EP, a.d, static_cast<__nv_bfloat16*>(wsplit),
-                                              p.ksplit > 1 ? p.tickets : nullptr, p.n_tiles);
-  count_launch();
-  cudaError_t e = cudaGetLastError();
+  int* tickets = p.ksplit > 1 ? p.tickets : nullptr;
+  cudaError_t e;
+  if (a.after_own) {
+    e = launch_pdl(split_router_kernel, dim3(sblocks), dim3(256), 0, s, a.W_r, a.E, EP, a.d,
+                   static_cast<__nv_bfloat16*>(wsplit), tickets, p.n_tiles);
+  } else {
+    split_router_kernel<<<sblocks, 256, 0, s>>>(a.W_r, a.E, EP, a.d, static_cast<__nv_bfloat16*>(wsplit), tickets, p.n_tiles);
+    count_launch();
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
   e = set_smem_limit_once(reinterpret_cast<const void*>(&router_tc_kernel<EP, K>), static_cast<int>(G::SMEM));
   if (e != cudaSuccess) return e;

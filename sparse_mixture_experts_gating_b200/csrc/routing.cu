@@ -824,6 +824,7 @@ __global__ void __launch_bounds__(256) route_small_dot_kernel(RoutingArgs a, int
     for (int wi = 0; wi < 8; ++wi) v += s_red[wi][tid];
     partial[(static_cast<int64_t>(ds) * T + tid) * a.E + e] = v;
   }
+  pdl_wait();  // (a.after_own: what waits for this grid waits for the one before too)
 }
 
 template <typename XT>
@@ -1162,12 +1163,18 @@ cudaError_t launch_route_small(const RoutingArgs& a, void* partials, cudaStream_
   const size_t smem = static_cast<size_t>(a.T) * a.E * sizeof(float);
   cudaError_t e;
   if (a.logits_in == nullptr) {  // the first kernel of the forward: an ordinary launch
-    if (a.x_is_bf16)
+    if (a.after_own)  // ... or the second, beside the first, whose own wait has seen to x
+      e = a.x_is_bf16 ? launch_pdl(route_small_dot_kernel<__nv_bfloat16>, dim3(n_ds, a.E), dim3(256), 0, s, a, chunk, part)
+                      : launch_pdl(route_small_dot_kernel<float>, dim3(n_ds, a.E), dim3(256), 0, s, a, chunk, part);
+    else if (a.x_is_bf16)
       route_small_dot_kernel<__nv_bfloat16><<<dim3(n_ds, a.E), 256, 0, s>>>(a, chunk, part);
     else
       route_small_dot_kernel<float><<<dim3(n_ds, a.E), 256, 0, s>>>(a, chunk, part);
-    count_launch();
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (!a.after_own) {
+      count_launch();
+      e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return e;
     if (a.x_is_bf16)
       return launch_pdl(route_small_kernel<__nv_bfloat16>, dim3(1), dim3(SCAN_T), smem, s, a, n_ds,
                         static_cast<const float*>(part));
