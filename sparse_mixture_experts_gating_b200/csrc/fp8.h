@@ -58,6 +58,7 @@ struct Fp8Args {
   int64_t ld_out;
   float* out_scales;       // activations, FP8_GATE_H16: [a_rows][ceil(N / 128)]
   int ksplit;
+  int cluster;             // > 1: K ranges summed within a cluster of CTAs (fp8_cluster), no partials
   int64_t split_stride;    // elements between the partials of consecutive K ranges
   int64_t pair_stride;     // FP8_PAIR_F32
   const float* row_gate;   // FP8_F32: may be NULL
@@ -66,7 +67,7 @@ struct Fp8Args {
 };
 
 struct Fp8Params {
-  int G, N, K, bn, n_tiles, num_kb, ksplit, kb_per;
+  int G, N, K, bn, n_tiles, num_kb, ksplit, kb_per, cluster;
   int64_t a_rows;
   const float* sa;
   int64_t sa_ld;
@@ -93,6 +94,9 @@ struct Fp8Plan {
 // output tiles alone cannot occupy the GPU.  summed_anyway: its partials cost no
 // launch of their own.
 int fp8_ksplit(int64_t rows, int G, int N, int K, bool summed_anyway = false);
+// The CTAs of a cluster that sum the `ksplit` K ranges of a product among
+// themselves; 1: the cut goes through partials and a second launch.
+int fp8_cluster(int64_t rows, int ksplit, int b_rows);
 cudaError_t plan_fp8(const Fp8Args& g, Fp8Plan* plan, const char** why);
 cudaError_t launch_fp8(const Fp8Plan& plan, int num_sms, cudaStream_t s);
 

@@ -107,7 +107,9 @@ int matmul_fp8(int64_t M, int64_t N, int64_t K, int64_t groups, const void* a_co
   unsigned int* err = nullptr;
   cudaError_t e = current_device_info(&num_sms, &err);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, F + cudaGetErrorString(e));
-  const int ks = need > 0 ? fp8_ksplit(M, static_cast<int>(groups), static_cast<int>(N), static_cast<int>(K)) : 1;
+  int ks = need > 0 ? fp8_ksplit(M, static_cast<int>(groups), static_cast<int>(N), static_cast<int>(K)) : 1;
+  const int cluster = fp8_cluster(M, ks, b_rows);
+  if (cluster > 1) ks = 1;  // (no partials)
   Fp8Args a;
   memset(&a, 0, sizeof(a));
   a.epi = ks > 1 || out_dtype == MOE_F32 ? FP8_F32 : FP8_BF16;
@@ -128,6 +130,7 @@ int matmul_fp8(int64_t M, int64_t N, int64_t K, int64_t groups, const void* a_co
   a.out = ks > 1 ? workspace : out;
   a.ld_out = ks > 1 ? partial_ld(N) : ld_out;
   a.ksplit = ks;
+  a.cluster = cluster;
   a.split_stride = ks > 1 ? M * partial_ld(N) : 0;
   a.offsets = offsets;
   a.err = err;

@@ -63,6 +63,9 @@ constexpr int EPI_WARPS = 8;
 constexpr int SB_ROWS = 12, SB_KB = 4, SB_LD = MMA_N + 8;
 constexpr uint32_t TMEM_COLS = 2 * MMA_N;
 constexpr int ROW_STAGE = 64;           // bytes per staged output row of a warp's own stores
+constexpr int CL_ROWS = 8;              // rows of a product whose CTAs may sum in clusters
+constexpr int CL_LD = MMA_N + 4;        // floats between the rows of a sum handed to the cluster's first CTA
+constexpr int MAX_CLUSTER = 8;
 constexpr int OUT_HALF = 2 * 16384;     // two boxes of 128 rows x 128 bytes of a warpgroup's TMA stores
 
 // AR: rows of A a stage holds.  No group has more rows than max_group_rows, so
@@ -267,6 +270,20 @@ __device__ __forceinline__ void mul_fma2(float& d0, float& d1, uint32_t a0, uint
       : "r"(a0), "r"(a1), "f"(b0), "f"(b1), "f"(s));
 }
 
+// Every thread of the cluster's CTAs meets here (what was written before is seen after).
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The address of p (this CTA's shared memory) in the cluster's first CTA, and a store to such an address.
+__device__ __forceinline__ uint32_t in_first_cta(const void* p) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+  return r;
+}
+__device__ __forceinline__ void st_cluster4(uint32_t at, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
+
 // acc[i] += t[i] * (a scale): one scale for all 32 columns, or (SB1) s times one for each in `b`.
 template <bool SB1>
 __device__ __forceinline__ void add32(float* acc, const uint32_t (&t)[32], float s, const float* b) {
@@ -316,13 +333,15 @@ struct OutWord { using type = uint16_t; };
 template <>
 struct OutWord<4> { using type = uint32_t; };
 
-template <int EPI, int AR, bool SB1>
+// CLUSTER: one item a CTA, its K ranges summed within a cluster (p.cluster CTAs).
+template <int EPI, int AR, bool SB1, bool CLUSTER>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
                     const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmOut, const Fp8Params p) {
   constexpr bool PAIR = EPI == FP8_SWIGLU || EPI == FP8_PAIR_F32;  // 128 columns of W1 and the same of W3
   constexpr bool F32 = EPI == FP8_F32 || EPI == FP8_PAIR_F32;
   constexpr bool ACT = EPI == FP8_SWIGLU || EPI == FP8_RELU;
+  static_assert(!CLUSTER || (AR < BM && (EPI == FP8_BF16 || EPI == FP8_F32)), "products of few rows");
   constexpr uint32_t IDESC = idesc_e4m3_f32(BM, MMA_N);
   using G = Geo<AR>;
   constexpr int STAGES = G::STAGES, STAGE_BYTES = G::STAGE_BYTES, A_ST = G::A_ST;
@@ -464,6 +483,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t col0 = PAIR ? 64u * half : 128u * half, col2 = PAIR ? 128u + 64u * half : 128u * half + 64u;
     int acc_i = 0, sb_row = 0;
+    bool met = false;  // CLUSTER
     uint32_t acc_phase = 0;
     bool ok = true;
     for (int64_t u = blockIdx.x; ok && item_at(ctl, p, u, w); u += gridDim.x) {
@@ -526,6 +546,30 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (SB1 && ++sb_row == SB_ROWS) sb_row = 0;
         if (++acc_i == 2) { acc_i = 0; acc_phase ^= 1u; }
         if (!ok) break;
+      }
+      // A cluster's CTAs hold the sums of their K ranges: the others' go to the
+      // first one, where the stages lay, and it adds them in order.  (One item a CTA.)
+      bool mine = true;
+      if constexpr (CLUSTER) {
+        cluster_meet();  // the first CTA's MMAs have read its stages
+        float* part = reinterpret_cast<float*>(stages) + r_in_tile * CL_LD + half * 128;
+        if (w.ks > 0 && vrow) {
+          const uint32_t to = in_first_cta(part + (w.ks - 1) * CL_ROWS * CL_LD);
+#pragma unroll
+          for (int i = 0; i < 128; i += 4) st_cluster4(to + i * 4, acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+        }
+        cluster_meet();
+        mine = w.ks == 0;
+        if (mine && vrow) {
+          for (int k = 1; k < p.cluster; ++k, part += CL_ROWS * CL_LD) {
+#pragma unroll
+            for (int i = 0; i < 128; i += 4) {
+              const float4 v = *reinterpret_cast<const float4*>(part + i);
+              acc[i] += v.x; acc[i + 1] += v.y; acc[i + 2] += v.z; acc[i + 3] += v.w;
+            }
+          }
+        }
+        met = true;
       }
       // Where warps meet at barriers, they leave an aborted CTA together.  (Also:
       // the last tile's hmax has been read, and its stores have read out_stage.)
@@ -630,7 +674,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             bulk_commit();
           }
         }
-      } else if (ok && warp_live) {
+      } else if (ok && warp_live && mine) {
         // through shared memory, so that the stores run along rows: 64 bytes of
         // every row at a time, or where the rows' alignment wants one element a
         // store, as many as there is room for
@@ -687,7 +731,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
     if (TMA_OUT && storer) bulk_wait();
+    if (CLUSTER && !met) { cluster_meet(); cluster_meet(); }
   }
+  if (CLUSTER && warp < 4) { cluster_meet(); cluster_meet(); }
 
   tc_fence_before();
   __syncthreads();
@@ -851,20 +897,30 @@ bool map_3d(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint64_
   return make_map_nd(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, 3, dims, strides, box);
 }
 
-template <int EPI, int AR, bool SB1>
+template <int EPI, int AR, bool SB1, bool CLUSTER = false>
 cudaError_t launch_t(const Fp8Plan& pl, int num_sms, cudaStream_t s) {
   constexpr size_t bytes = smem_bytes<AR, SB1>();
   static_assert(bytes <= 227 * 1024, "8-bit product: shared memory");
-  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(&fp8_gemm_kernel<EPI, AR, SB1>),
-                                      static_cast<int>(bytes));
+  auto* kernel = fp8_gemm_kernel<EPI, AR, SB1, CLUSTER>;
+  const cudaError_t e = set_smem_limit_once(reinterpret_cast<const void*>(kernel), static_cast<int>(bytes));
   if (e != cudaSuccess) return e;
-  return launch_pdl(fp8_gemm_kernel<EPI, AR, SB1>, dim3(num_sms), dim3(NUM_THREADS), bytes, s, pl.a, pl.b0, pl.b1, pl.out, pl.p);
+  if constexpr (CLUSTER) {
+    static_assert(Geo<AR>::STAGES * Geo<AR>::STAGE_BYTES >= (MAX_CLUSTER - 1) * CL_ROWS * CL_LD * 4, "the sums' room");
+    // groups of so few rows have one row tile each
+    const int64_t tiles = std::min<int64_t>(pl.p.G, pl.p.a_rows) * pl.p.n_tiles;
+    return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(tiles * pl.p.cluster)), pl.p.cluster, dim3(NUM_THREADS),
+                              bytes, s, pl.a, pl.b0, pl.b1, pl.out, pl.p);
+  } else {
+    return launch_pdl(kernel, dim3(num_sms), dim3(NUM_THREADS), bytes, s, pl.a, pl.b0, pl.b1, pl.out, pl.p);
+  }
 }
 
 template <int EPI>
 cudaError_t launch_ar(const Fp8Plan& pl, int num_sms, cudaStream_t s) {
-  if constexpr (EPI == FP8_BF16 || EPI == FP8_F32)
+  if constexpr (EPI == FP8_BF16 || EPI == FP8_F32) {
+    if (pl.p.cluster > 1) return launch_t<EPI, 32, false, true>(pl, num_sms, s);  // (CL_ROWS rows at most)
     if (pl.sb1) return launch_t<EPI, 128, true>(pl, num_sms, s);
+  }
   if (pl.ar == 32) return launch_t<EPI, 32, false>(pl, num_sms, s);
   if (pl.ar == 64) return launch_t<EPI, 64, false>(pl, num_sms, s);
   return launch_t<EPI, 128, false>(pl, num_sms, s);
@@ -914,6 +970,13 @@ int fp8_ksplit(int64_t rows, int G, int N, int K, bool summed_anyway) {
   return static_cast<int>(best);
 }
 
+int fp8_cluster(int64_t rows, int ksplit, int b_rows) {
+  // 8 rows, 14336 x 4096 in two ranges: 13.1 us, by partials and a second launch 15.3
+  // us; 2048 x 768 in three: 6.5 and 8.3 us (weights in L2).  16 rows tie, and
+  // 64 rows' sums take an SM 4 us to receive.
+  return rows <= CL_ROWS && b_rows != 1 && ksplit >= 2 && ksplit <= MAX_CLUSTER ? ksplit : 1;
+}
+
 cudaError_t plan_fp8(const Fp8Args& g, Fp8Plan* pl, const char** why) {
   *why = nullptr;
   const bool pair = g.epi == FP8_SWIGLU || g.epi == FP8_PAIR_F32;
@@ -942,6 +1005,8 @@ cudaError_t plan_fp8(const Fp8Args& g, Fp8Plan* pl, const char** why) {
   p.n_tiles = (g.N + p.bn - 1) / p.bn;
   p.num_kb = (g.K + BK - 1) / BK;
   p.ksplit = g.epi == FP8_F32 || g.epi == FP8_PAIR_F32 ? std::max(1, std::min(g.ksplit, p.num_kb)) : 1;
+  p.cluster = std::max(1, g.cluster);
+  if (p.cluster > 1) p.ksplit = p.cluster;
   p.kb_per = (p.num_kb + p.ksplit - 1) / p.ksplit;
   p.a_rows = g.a_rows;
   p.sa = g.sa;
@@ -956,7 +1021,7 @@ cudaError_t plan_fp8(const Fp8Args& g, Fp8Plan* pl, const char** why) {
   p.out_scales = g.out_scales;
   const int elt = g.epi == FP8_BF16 || g.epi == FP8_GATE_H16 ? 2 : 4;
   // (a partial's rows have room behind N for the last piece)
-  const bool whole_n = g.epi == FP8_F32 && p.ksplit > 1 && g.ld_out >= (g.N + 3) / 4 * 4;
+  const bool whole_n = g.epi == FP8_F32 && p.ksplit > 1 && p.cluster == 1 && g.ld_out >= (g.N + 3) / 4 * 4;
   p.vec_out = ((reinterpret_cast<uintptr_t>(g.out) | static_cast<uintptr_t>(g.ld_out * elt) |
                 static_cast<uintptr_t>(whole_n ? 0 : static_cast<int64_t>(g.N) * elt) | static_cast<uintptr_t>(g.split_stride * elt) |
                 static_cast<uintptr_t>(g.pair_stride * elt)) & 15) == 0;

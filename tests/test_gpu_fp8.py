@@ -185,6 +185,31 @@ def test_grouped_product_of_long_rows_and_many_groups(M, N, K, G, out_dtype, b_r
     assert (out[:cuts[0]] == 7).all() and (out[cuts[-1]:] == 7).all()
 
 
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+@pytest.mark.parametrize("M,N,K,G", [(1, 14000, 640, None), (5, 4096, 4100, None), (32, 2001, 2048, None), (64, 4096, 1024, None),
+                                     (33, 2900, 2048, None), (64, 777, 1500, None), (20, 4100, 2048, 5), (50, 1024, 1152, 9),
+                                     (7, 2000, 4096, 30), (8, 3333, 1025, None), (8, 4100, 2048, 3), (2, 14080, 384, 2),
+                                     (3, 3585, 5000, None)])
+def test_few_rows_whose_sums_meet_in_a_cluster(M, N, K, G, out_dtype):
+    """K cut over the CTAs of a cluster, dense and grouped (with empty groups and rows of none)."""
+    a, b = operands(M, N, K, G, 128, M + N)
+    out = torch.full((M, N), 7.0, dtype=out_dtype, device="cuda")
+    if G is None:
+        matmul_fp8(a, b, out_dtype=out_dtype, out=out)
+        status()
+        check_product(out, host(a, 1), host(b, 128), out_dtype)
+        return
+    cuts = np.sort(np.random.default_rng(M).integers(0, M + 1, G + 1))
+    matmul_fp8(a, b, offsets=torch.from_numpy(cuts.astype(np.int32)).cuda(), out_dtype=out_dtype, out=out)
+    status()
+    av, bc, bs = host(a, 1), code_values(b[0]), b[1].cpu().numpy()
+    for g in range(G):
+        lo, hi = cuts[g], cuts[g + 1]
+        if hi > lo:
+            check_product(out[lo:hi], av[lo:hi], F.values(bc[g], bs[g], 128), out_dtype)
+    assert (out[:cuts[0]] == 7).all() and (out[cuts[-1]:] == 7).all()
+
+
 def test_product_writes_its_columns_only():
     """A result with a wider row stride, and one that starts at an odd element."""
     a, b = operands(140, 77, 256, None, 128, 5)
