@@ -10,11 +10,12 @@
 // multiply by sa * sb and add it to fp32 registers while the next k-block's
 // MMAs fill the other accumulator.  Tiles are 128 rows x 256 columns.
 //
-// What bounds it: a k-block's MMAs take 514 cycles, its 32768 additions 256 (the
-// fp32 rate of an SM) and its read-back 144, which add up to 320-400 in a loop
-// of nothing else; with the barriers, scales and moves between registers a
-// k-block takes about 900.  8192 x 14336 x 4096: 456 us in bursts (2.1
-// PFLOP/s), 507-520 us back to back, where the board's power limit sets the
+// What bounds it: alone, a k-block's MMAs take 514 cycles, its 32768 additions 256
+// (the fp32 rate of an SM) and its read-back 144.  Together a k-block takes 930:
+// the MMAs 720 (48 KB that TMA writes and 48 KB that they read are 750 cycles of
+// shared memory), the summing warps 730 and a wait of 200, for the read-back
+// shares TMEM with the accumulation.  8192 x 14336 x 4096: 456 us in bursts (2.1
+// PFLOP/s), 507-541 us back to back, where the board's power limit sets the
 // clock (cuBLAS with one scale per tensor: 331 and 385 us).  Eight summing warps
 // of 128 columns with 232 registers each were the fastest of the forms tried;
 // sixteen of 64 columns, MMAs of half the width with four accumulators, and

@@ -9,6 +9,10 @@
 // without a special case; 448 / a stays finite down to a = 2^-100.  A NaN
 // keeps the NaN code; an infinity makes its block's scale infinite, so that
 // the whole block reads back as NaN.
+//
+// What bounds it: HBM.  bf16, 8192 x 4096: rows 19.5 us (5.2 TB/s, 2 us of it the
+// launch), transposed rows 22.9 us, transposed blocks 18.7 us; 128 x 768 x 2048 in
+// blocks 96 us (6.4 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
