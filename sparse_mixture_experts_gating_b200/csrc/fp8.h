@@ -96,7 +96,7 @@ struct Fp8Plan {
 int fp8_ksplit(int64_t rows, int G, int N, int K, bool summed_anyway = false);
 // The CTAs of a cluster that sum the `ksplit` K ranges of a product among
 // themselves; 1: the cut goes through partials and a second launch.
-int fp8_cluster(int64_t rows, int ksplit, int b_rows);
+int fp8_cluster(int64_t rows, int ksplit, int K, int b_rows);
 cudaError_t plan_fp8(const Fp8Args& g, Fp8Plan* plan, const char** why);
 cudaError_t launch_fp8(const Fp8Plan& plan, int num_sms, cudaStream_t s);
 

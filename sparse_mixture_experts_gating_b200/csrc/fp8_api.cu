@@ -108,7 +108,7 @@ int matmul_fp8(int64_t M, int64_t N, int64_t K, int64_t groups, const void* a_co
   cudaError_t e = current_device_info(&num_sms, &err);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, F + cudaGetErrorString(e));
   int ks = need > 0 ? fp8_ksplit(M, static_cast<int>(groups), static_cast<int>(N), static_cast<int>(K)) : 1;
-  const int cluster = fp8_cluster(M, ks, b_rows);
+  const int cluster = fp8_cluster(M, ks, static_cast<int>(K), b_rows);
   if (cluster > 1) ks = 1;  // (no partials)
   Fp8Args a;
   memset(&a, 0, sizeof(a));

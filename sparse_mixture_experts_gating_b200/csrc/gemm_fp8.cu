@@ -12,9 +12,9 @@
 //
 // What bounds it: alone, a k-block's MMAs take 514 cycles, its 32768 additions 256
 // (the fp32 rate of an SM) and its read-back 144.  Together a k-block takes 930:
-// the MMAs 720 (48 KB that TMA writes and 48 KB that they read are 750 cycles of
-// shared memory), the summing warps 730 and a wait of 200, for the read-back
-// shares TMEM with the accumulation.  8192 x 14336 x 4096: 456 us in bursts (2.1
+// the MMAs 720, the summing warps 730 and a wait of 200, for the read-back shares
+// TMEM with the accumulation (counters: tensor pipe 54 % active, shared memory's
+// banks 20 % reads and 20 % writes).  8192 x 14336 x 4096: 456 us in bursts (2.1
 // PFLOP/s), 507-541 us back to back, where the board's power limit sets the
 // clock (cuBLAS with one scale per tensor: 331 and 385 us).  Eight summing warps
 // of 128 columns with 232 registers each were the fastest of the forms tried;
@@ -971,11 +971,17 @@ int fp8_ksplit(int64_t rows, int G, int N, int K, bool summed_anyway) {
   return static_cast<int>(best);
 }
 
-int fp8_cluster(int64_t rows, int ksplit, int b_rows) {
+int fp8_cluster(int64_t rows, int ksplit, int K, int b_rows) {
   // 8 rows, 14336 x 4096 in two ranges: 13.1 us, by partials and a second launch 15.3
   // us; 2048 x 768 in three: 6.5 and 8.3 us (weights in L2).  16 rows tie, and
-  // 64 rows' sums take an SM 4 us to receive.
-  return rows <= CL_ROWS && b_rows != 1 && ksplit >= 2 && ksplit <= MAX_CLUSTER ? ksplit : 1;
+  // 64 rows' sums take an SM 4 us to receive.  More ranges than a cluster has
+  // CTAs pay for their second launch from about three k-blocks less a range on
+  // (2048 x 4096, 12 ranges of 3 or 8 of 4: 9.0 and 8.7 us; 768 x 8192, 32 of 2
+  // or 8 of 8: 9.8 and 10.1 us).
+  if (rows > CL_ROWS || b_rows == 1 || ksplit < 2) return 1;
+  const int num_kb = (K + BK - 1) / BK, c = std::min(ksplit, MAX_CLUSTER);
+  const int per = (num_kb + c - 1) / c, per_cut = (num_kb + ksplit - 1) / ksplit;
+  return per <= per_cut + 3 ? (num_kb + per - 1) / per : 1;
 }
 
 cudaError_t plan_fp8(const Fp8Args& g, Fp8Plan* pl, const char** why) {

@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 from typing import Optional
 
@@ -65,6 +66,16 @@ def _on(index: int, stream):
     if stream is None and torch._C._cuda_getDevice() == index:
         return _Here(torch._C._cuda_getCurrentRawStream(index))
     return _switched(index, stream)
+
+
+@functools.lru_cache(maxsize=4096)
+def _matmul_workspace(M: int, N: int, K: int, G: int) -> int:
+    return int(lib().moe_matmul_fp8_workspace_bytes(M, N, K, G))
+
+
+@functools.lru_cache(maxsize=4096)
+def _balance_workspace(T: int, E: int, B: int) -> int:
+    return int(lib().moe_router_balance_workspace_bytes(T, E, B))
 
 
 def _blocks(n: int) -> int:
@@ -432,10 +443,9 @@ def matmul_fp8(a, b, *, offsets: Optional[torch.Tensor] = None, out_dtype=torch.
     with _on(dev, stream) as handle:
         if out is None:
             out = sa.new_empty((M, N), dtype=out_dtype)
-        L = lib()
-        n = L.moe_matmul_fp8_workspace_bytes(M, N, K, G)
+        n = _matmul_workspace(M, N, K, G)
         ws = sa.new_empty(n, dtype=torch.uint8) if n else None
-        check(L.moe_matmul_fp8(M, N, K, G, ac.data_ptr(), fa[3], sa.data_ptr(), bc.data_ptr(), fb[3], sb.data_ptr(),
+        check(lib().moe_matmul_fp8(M, N, K, G, ac.data_ptr(), fa[3], sa.data_ptr(), bc.data_ptr(), fb[3], sb.data_ptr(),
                                b_rows, None if offsets is None else offsets.data_ptr(), out.data_ptr(), out_kind, ld_out,
                                None if ws is None else ws.data_ptr(), n, handle))
     return out
@@ -471,10 +481,9 @@ def router_balance(logits: torch.Tensor, k: int, *, offsets: Optional[torch.Tens
     with _on(dev, stream) as handle:
         f32, i32, new = torch.float32, torch.int32, logits.new_empty
         aux, z, counts, tokens = new(B, dtype=f32), new(B, dtype=f32), new((B, E), dtype=i32), new(B, dtype=i32)
-        L = lib()
-        n = L.moe_router_balance_workspace_bytes(T, E, B)
+        n = _balance_workspace(T, E, B)
         ws = new(n, dtype=torch.uint8)
-        check(L.moe_router_balance(T, E, k, logits.data_ptr(), DTYPE[logits.dtype], SCORING[scoring], B,
+        check(lib().moe_router_balance(T, E, k, logits.data_ptr(), DTYPE[logits.dtype], SCORING[scoring], B,
                                    None if offsets is None else offsets.data_ptr(),
                                    None if mask is None else mask.data_ptr(), aux.data_ptr(), z.data_ptr(),
                                    counts.data_ptr(), tokens.data_ptr(), ws.data_ptr(), n, handle))

@@ -151,12 +151,9 @@ def test_ties_go_to_the_lower_index():
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
-@pytest.mark.parametrize("E", [1, 2, 5, 8, 9, 16, 31, 64, 100, 256])
-@pytest.mark.parametrize("k", [1, 2, 4, 8])
+@pytest.mark.parametrize("E,k", [(E, k) for E in (1, 2, 5, 8, 9, 16, 31, 64, 100, 256) for k in (1, 2, 4, 8) if k <= E])
 def test_rows_of_few_values(E, k, dtype):
     """Logits all alike, or of two or three values, with some experts at -inf."""
-    if k > E:
-        pytest.skip("k <= E")
     g = torch.Generator(device="cuda").manual_seed(E * 10 + k)
     l = torch.randint(0, 3, (240, E), device="cuda", generator=g).float()
     l[:80] = 0.0

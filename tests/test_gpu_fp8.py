@@ -189,7 +189,8 @@ def test_grouped_product_of_long_rows_and_many_groups(M, N, K, G, out_dtype, b_r
 @pytest.mark.parametrize("M,N,K,G", [(1, 14000, 640, None), (5, 4096, 4100, None), (32, 2001, 2048, None), (64, 4096, 1024, None),
                                      (33, 2900, 2048, None), (64, 777, 1500, None), (20, 4100, 2048, 5), (50, 1024, 1152, 9),
                                      (7, 2000, 4096, 30), (8, 3333, 1025, None), (8, 4100, 2048, 3), (2, 14080, 384, 2),
-                                     (3, 3585, 5000, None)])
+                                     (3, 3585, 5000, None), (1, 256, 4096, None), (8, 130, 7100, None), (4, 1500, 4096, 2),
+                                     (2, 100, 15000, None)])
 def test_few_rows_whose_sums_meet_in_a_cluster(M, N, K, G, out_dtype):
     """K cut over the CTAs of a cluster, dense and grouped (with empty groups and rows of none)."""
     a, b = operands(M, N, K, G, 128, M + N)
