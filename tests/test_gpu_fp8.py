@@ -211,6 +211,31 @@ def test_few_rows_whose_sums_meet_in_a_cluster(M, N, K, G, out_dtype):
     assert (out[:cuts[0]] == 7).all() and (out[cuts[-1]:] == 7).all()
 
 
+def test_cluster_products_captured_and_on_two_streams():
+    a, b = operands(2, 2000, 4096, None, 128, 21)
+    a2, _ = operands(2, 2000, 4096, None, 128, 22)
+    x = [t.clone() for t in a]
+    ref, ref2 = matmul_fp8(a, b), matmul_fp8(a2, b)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        out = matmul_fp8(x, b)
+    for src, want in ((a, ref), (a2, ref2), (a, ref)):
+        for t, s in zip(x, src):
+            t.view(torch.uint8).copy_(s.view(torch.uint8))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [matmul_fp8(p, b, stream=s) for _ in range(20) for p, s in zip((a, a2), streams)]
+    torch.cuda.synchronize()
+    status()
+    for i, y in enumerate(got):
+        assert torch.equal(y, (ref, ref2)[i % 2])
+
+
 def test_product_writes_its_columns_only():
     """A result with a wider row stride, and one that starts at an odd element."""
     a, b = operands(140, 77, 256, None, 128, 5)
