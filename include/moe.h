@@ -298,7 +298,8 @@ MOE_API int moe_forward_w4(moe_handle h, int64_t T, const void* x, const float* 
  * reads x itself; the experts read x and the hidden activation quantised with
  * block_rows 1.  Arguments, results and errors as moe_forward; W3_codes and
  * W3_scales are NULL for ReLU layers; the workspace is
- * moe_workspace_bytes_fp8(h, T) bytes.  moe_backward does not serve layers run
+ * moe_workspace_bytes_fp8(h, T) bytes.  A NaN of the first projection stays one
+ * under both activations (ReLU in moe_forward and moe_forward_w4 gives 0).  moe_backward does not serve layers run
  * this way.
  */
 MOE_API int moe_quantize_fp8(const void* x, int dtype, int64_t matrices, int64_t rows, int64_t K, int64_t ld,

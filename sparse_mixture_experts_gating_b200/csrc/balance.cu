@@ -41,12 +41,6 @@ constexpr int THREADS = 256;
 // A slot holds psum [E], counts [E], sum of lse^2, tokens.
 __host__ __device__ inline int slot_words(int E) { return 2 * E + 2; }
 
-__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 template <int W>
 __device__ __forceinline__ float group_max(float v) {
 #pragma unroll

@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         float m = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          acc[i] = PAIR ? silu_mul(acc[i], acc[(i + 64) & 127]) : fmaxf(acc[i], 0.f);
+          acc[i] = PAIR ? silu_mul(acc[i], acc[(i + 64) & 127]) : max_nan(acc[i], 0.f);
           m = fmaxf(m, fabsf(acc[i]));
         }
         if (n0 + NV > p.N) {  // columns past N are not the row's
@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(256) fp8_hidden_kernel(const Fp8HiddenArgs a) 
     float m = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      v[j] = PAIR ? silu_mul(v[j], u[j]) : fmaxf(v[j], 0.f);
+      v[j] = PAIR ? silu_mul(v[j], u[j]) : max_nan(v[j], 0.f);
       m = fmaxf(m, fabsf(v[j]));
     }
 #pragma unroll

@@ -256,3 +256,28 @@ def test_empty_batch_and_refusals():
             call()
     with pytest.raises(MoEError):  # a SwiGLU layer without W3
         layer.forward_fp8(x, W_r, None, q["W1"], None, q["W2"])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")], ids=["nan", "inf"])
+@pytest.mark.parametrize("T,d,d_ff", [(3, 2048, 128), (50, 256, 384), (100, 2048, 256), (200, 128, 272)],
+                         ids=["cut_few_rows", "few_rows", "cut_tiles", "whole_tiles"])
+@pytest.mark.parametrize("act", [R, S], ids=["relu", "swiglu"])
+def test_a_weight_that_is_not_finite_reaches_the_tokens_of_its_expert(act, T, d, d_ff, bad):
+    """A NaN of the first projection stays one under both activations: y is NaN for
+    the tokens that the expert serves, and for no other."""
+    w = Workload("not_finite", T=T, d=d, E=4, k=2, d_ff=d_ff, act=act, gate=RN, capacity_factor=0.0, dtype=DTYPE_BF16,
+                 dyadic=True, seed=53)
+    inp = make_inputs(w, device="cuda")
+    layer = layer_for(w)
+    dbg = layer.debug_buffers(T, "cuda")
+    q = quantized(inp)
+    layer.forward_fp8(inp["x"], inp["W_r"], inp["b_r"], q["W1"], q["W3"], q["W2"], debug=dbg)
+    e = int(dbg["topk_idx"][0, 1])  # an expert that some token takes
+    inp["W1"][e, d_ff - 3, d // 2 + 1] = bad
+    q = quantized(inp)
+    y, *_ = layer.forward_fp8(inp["x"], inp["W_r"], inp["b_r"], q["W1"], q["W3"], q["W2"])
+    status()
+    served = (dbg["topk_idx"] == e).any(1)
+    assert served.any()
+    assert torch.equal(torch.isnan(y), served[:, None].expand(T, d))
+    assert torch.isfinite(y[~served]).all()
