@@ -145,7 +145,7 @@ class MoELayer:
         self._h = h
         self._ws = None
         self._bw = None  # backward scratch
-        self._last = None  # the workspace of forward_fp8's last call without one of the caller's
+        self._last = None  # the workspace of forward_fp8, where the last call without one of the caller's was its
         self.hidden = hidden
         check(lib().moe_set_hidden_precision(h, HIDDEN[hidden]))
         self.n_shared = int(n_shared)
@@ -278,9 +278,13 @@ class MoELayer:
                  bw_workspace=None, grads=None, stream=None, dlogits=None) -> dict:
         """Gradients of <dy, y> + aux_coef * aux + z_coef * z for the last
         forward on ``workspace`` (default: this layer's own), routing held
-        fixed.  dlogits [T, E] fp32: a further gradient of the router logits
+        fixed.  It does not serve forward_fp8: refused without ``workspace``
+        where that was the layer's last.  dlogits [T, E] fp32: a further gradient of the router logits
         (router_balance_backward makes one).  Returns fp32 device tensors dx, dW_r, db_r (None without a
         bias), dW1, dW3 (None for ReLU), dW2; ``grads`` may supply them."""
+        if workspace is None and self._last is not None:
+            raise ValueError("backward: the layer's last forward was forward_fp8, which it does not serve; "
+                             "run forward() again, or pass the workspace of the one that is meant")
         T, dev = x.shape[0], x.device
         ws = workspace if workspace is not None else self._ws
         if bw_workspace is None:

@@ -258,3 +258,12 @@ def test_balance_gradient_matches_differences(scoring):
                 a, z, *_ = D.loss(x, k, cuts, mask, scoring, hot)
                 v.append((daux * a).sum() + (dz * z).sum())
             assert abs((v[0] - v[1]) / 2e-6 - d[t, e]) < 1e-7
+
+
+def test_backward_refuses_a_layer_whose_last_forward_was_8_bit():
+    """(The refusal is made before anything is read: tensors on the CPU do.)"""
+    layer = moe.MoELayer(4, 2, 64, 64)
+    x, W_r, W = torch.zeros(8, 64), torch.zeros(4, 64), torch.zeros(4, 64, 64)
+    layer._last = torch.zeros(256, dtype=torch.uint8)  # as forward_fp8 leaves it
+    with pytest.raises(ValueError, match="forward_fp8"):
+        layer.backward(x, W_r, None, W, W, W, x)

@@ -281,3 +281,27 @@ def test_a_weight_that_is_not_finite_reaches_the_tokens_of_its_expert(act, T, d,
     assert served.any()
     assert torch.equal(torch.isnan(y), served[:, None].expand(T, d))
     assert torch.isfinite(y[~served]).all()
+
+
+def test_backward_after_an_8_bit_forward():
+    """Refused without a workspace; with the one of a forward, and after another
+    forward, it gives that forward's gradients."""
+    w = CASES[1]
+    inp = make_inputs(w, device="cuda")
+    q = quantized(inp)
+    layer = layer_for(w)
+    args = [inp[n] for n in ("x", "W_r", "b_r", "W1", "W3", "W2")]
+    dy = torch.ones_like(inp["x"])
+    layer.forward(*args)
+    want = layer.backward(*args, dy)
+    ws = torch.empty(layer.workspace_bytes(w.T), dtype=torch.uint8, device="cuda")
+    layer.forward(*args, workspace=ws)
+    layer.forward_fp8(inp["x"].flip(0), inp["W_r"], inp["b_r"], q["W1"], q["W3"], q["W2"])
+    with pytest.raises(ValueError, match="forward_fp8"):
+        layer.backward(*args, dy)
+    kept = layer.backward(*args, dy, workspace=ws)
+    layer.forward(*args)
+    again = layer.backward(*args, dy)
+    status()
+    for name, g in want.items():
+        assert g is None or (torch.equal(g, kept[name]) and torch.equal(g, again[name])), name
