@@ -943,12 +943,14 @@ int fp8_ksplit(int64_t rows, int G, int N, int K, bool summed_anyway) {
     // HBM gives (a k-block takes a CTA 0.45 us, 73 GB/s).  One token times 14336 x
     // 4096, 56 tiles: uncut 19.8 us, cut in two 18.2 us, in five 20.7 us, each
     // with the second launch; 224 tiles, two experts' first projections: uncut 52
-    // us, cut in three 57 us.
+    // us, cut in three 57 us.  The ranges stay within one wave of CTAs: 86 tiles
+    // (one token times 22016 x 4096) cut in two, 172 ranges, take 27.4 us, uncut 20.7.
     // Where a launch that follows sums the partials anyway, a cut is free, and
     // fills the SMs (one token's second projections, 32 tiles: three ranges 30.0 us,
     // four 29.4 us).
     if (!summed_anyway && tiles >= 96) return 1;
-    const int64_t want = summed_anyway ? std::max<int64_t>(kSplitTargetCtas / tiles, 1) : (96 + tiles - 1) / tiles;
+    const int64_t wave = std::max<int64_t>(kSplitTargetCtas / tiles, 1);
+    const int64_t want = summed_anyway ? wave : std::min((96 + tiles - 1) / tiles, wave);
     const int64_t ks = std::min(want, std::max<int64_t>(num_kb / 2, 1));
     const int64_t per = (num_kb + ks - 1) / ks;
     return static_cast<int>((num_kb + per - 1) / per);

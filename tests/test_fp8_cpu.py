@@ -267,3 +267,18 @@ def test_backward_refuses_a_layer_whose_last_forward_was_8_bit():
     layer._last = torch.zeros(256, dtype=torch.uint8)  # as forward_fp8 leaves it
     with pytest.raises(ValueError, match="forward_fp8"):
         layer.backward(x, W_r, None, W, W, W, x)
+
+
+def test_a_cut_of_few_rows_stays_within_one_wave(L):
+    """Products of at most 64 rows: the K ranges of all tiles together are no more
+    than an SM has one of (148); from 75 to 95 tiles there is one range a tile."""
+    for groups in (1, 2, 8):
+        for M in (1, 3, 8, 16, 64):
+            used = min(groups, M)
+            for per_group in range(1, 150):
+                N, tiles = per_group * 256, per_group * used
+                n = L.moe_matmul_fp8_workspace_bytes(M, N, 4096, groups)
+                ranges = max(1, n // (4 * M * N))
+                assert n == (0 if ranges == 1 else 4 * M * N * ranges)
+                assert ranges == 1 or tiles * ranges <= 148, (groups, M, N)
+                assert ranges == 1 or tiles < 75, (groups, M, N)
