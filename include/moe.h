@@ -289,8 +289,9 @@ MOE_API int moe_forward_w4(moe_handle h, int64_t T, const void* x, const float* 
  *   4-byte aligned; 1 <= groups <= 256; M may be 0, N and K at least 1.  The
  *   product of two scales must be a normal fp32 number.  Offsets outside [0,
  *   M] or not ascending give wrong rows, never an access outside the buffers.
- *   workspace: moe_matmul_fp8_workspace_bytes(M, N, K, groups) bytes (may be
- *   0), 256-byte aligned.
+ *   workspace: moe_matmul_fp8_scratch_bytes(M, N, K, groups, b_rows) bytes (may
+ *   be 0, then NULL will do), 256-byte aligned;
+ *   moe_matmul_fp8_workspace_bytes(M, N, K, groups) is enough for either b_rows.
  *
  * moe_forward_fp8: moe_forward of a bf16 layer (d and d_ff multiples of 16)
  * whose expert weights are given in that format, block_rows 128, contiguous:
@@ -306,6 +307,7 @@ MOE_API int moe_quantize_fp8(const void* x, int dtype, int64_t matrices, int64_t
                              int block_rows, int transpose, void* codes, int64_t ld_codes, float* scales,
                              void* stream);
 MOE_API size_t moe_matmul_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t groups);
+MOE_API size_t moe_matmul_fp8_scratch_bytes(int64_t M, int64_t N, int64_t K, int64_t groups, int b_rows);
 MOE_API int moe_matmul_fp8(int64_t M, int64_t N, int64_t K, int64_t groups, const void* a_codes, int64_t lda,
                            const float* a_scales, const void* b_codes, int64_t ldb, const float* b_scales, int b_rows,
                            const int32_t* offsets, void* out, int out_dtype, int64_t ld_out, void* workspace,

@@ -48,6 +48,7 @@ SIGNATURES = {
     "moe_quantize_fp8": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_int64, c_int, c_int, c_void_p,
                                  c_int64, c_void_p, c_void_p]),
     "moe_matmul_fp8_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64, c_int64]),
+    "moe_matmul_fp8_scratch_bytes": (c_size_t, [c_int64, c_int64, c_int64, c_int64, c_int]),
     "moe_matmul_fp8": (c_int, [c_int64, c_int64, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_int64,
                                c_void_p, c_int, c_void_p, c_void_p, c_int, c_int64, c_void_p, c_size_t, c_void_p]),
     "moe_workspace_bytes_fp8": (c_size_t, [c_void_p, c_int64]),

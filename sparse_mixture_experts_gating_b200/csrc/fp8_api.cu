@@ -37,6 +37,25 @@ bool product_too_large(int64_t M, int64_t N, int64_t K, int64_t groups) {
          (M / 128 + groups) * ceil_div(N, 128) > 2147483647LL;
 }
 
+// How a product's K is cut: into `ranges` whose partials a second launch adds,
+// or (ranges 1) among the `cluster` CTAs of a cluster, without partials.
+struct Cut {
+  int ranges, cluster;
+};
+Cut cut_of(int64_t M, int64_t N, int64_t K, int64_t groups, int b_rows) {
+  const int ks = fp8_ksplit(M, static_cast<int>(groups), static_cast<int>(N), static_cast<int>(K));
+  const int cluster = fp8_cluster(M, ks, static_cast<int>(K), b_rows);
+  return {cluster > 1 ? 1 : ks, cluster};
+}
+
+size_t partial_bytes(int64_t M, int64_t N, int ranges) {
+  return ranges > 1 ? sizeof(float) * static_cast<size_t>(ranges) * static_cast<size_t>(M) * static_cast<size_t>(partial_ld(N)) : 0;
+}
+
+bool has_plan(int64_t M, int64_t N, int64_t K, int64_t groups) {
+  return M > 0 && N > 0 && K > 0 && groups > 0 && groups <= kFp8MaxGroups && !product_too_large(M, N, K, groups);
+}
+
 int quantize_fp8(const void* x, int dtype, int64_t matrices, int64_t rows, int64_t K, int64_t ld, int block_rows,
                      int transpose, void* codes, int64_t ld_codes, float* scales, void* stream) {
   const std::string F = "moe_quantize_fp8: ";
@@ -99,17 +118,16 @@ int matmul_fp8(int64_t M, int64_t N, int64_t K, int64_t groups, const void* a_co
     return fail(MOE_ERR_INVALID_ARG, F + "codes and their row strides must be multiples of 16 bytes");
   if (!aligned(a_scales, 4) || !aligned(b_scales, 4) || !aligned(offsets, 4) || !aligned(out, out_dtype == MOE_BF16 ? 2 : 4))
     return fail(MOE_ERR_INVALID_ARG, F + "scales, offsets and out must be aligned to their elements");
-  const size_t need = moe_matmul_fp8_workspace_bytes(M, N, K, groups);
+  const Cut cut = cut_of(M, N, K, groups, b_rows);
+  const size_t need = partial_bytes(M, N, cut.ranges);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256)))
     return fail(MOE_ERR_INVALID_ARG, F + "workspace missing, not 256-byte aligned or smaller than "
-                                         "moe_matmul_fp8_workspace_bytes()");
+                                         "moe_matmul_fp8_scratch_bytes()");
   int num_sms = 0;
   unsigned int* err = nullptr;
   cudaError_t e = current_device_info(&num_sms, &err);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, F + cudaGetErrorString(e));
-  int ks = need > 0 ? fp8_ksplit(M, static_cast<int>(groups), static_cast<int>(N), static_cast<int>(K)) : 1;
-  const int cluster = fp8_cluster(M, ks, static_cast<int>(K), b_rows);
-  if (cluster > 1) ks = 1;  // (no partials)
+  const int ks = cut.ranges;
   Fp8Args a;
   memset(&a, 0, sizeof(a));
   a.epi = ks > 1 || out_dtype == MOE_F32 ? FP8_F32 : FP8_BF16;
@@ -130,7 +148,7 @@ int matmul_fp8(int64_t M, int64_t N, int64_t K, int64_t groups, const void* a_co
   a.out = ks > 1 ? workspace : out;
   a.ld_out = ks > 1 ? partial_ld(N) : ld_out;
   a.ksplit = ks;
-  a.cluster = cluster;
+  a.cluster = cut.cluster;
   a.split_stride = ks > 1 ? M * partial_ld(N) : 0;
   a.offsets = offsets;
   a.err = err;
@@ -173,9 +191,12 @@ int moe_quantize_fp8(const void* x, int dtype, int64_t matrices, int64_t rows, i
 }
 
 size_t moe_matmul_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t groups) {
-  if (M <= 0 || N <= 0 || K <= 0 || groups <= 0 || groups > kFp8MaxGroups || product_too_large(M, N, K, groups)) return 0;
-  const int ks = fp8_ksplit(M, static_cast<int>(groups), static_cast<int>(N), static_cast<int>(K));
-  return ks > 1 ? sizeof(float) * static_cast<size_t>(ks) * static_cast<size_t>(M) * static_cast<size_t>(partial_ld(N)) : 0;
+  return moe_matmul_fp8_scratch_bytes(M, N, K, groups, 1);  // (never summed in clusters)
+}
+
+size_t moe_matmul_fp8_scratch_bytes(int64_t M, int64_t N, int64_t K, int64_t groups, int b_rows) {
+  if (!has_plan(M, N, K, groups) || (b_rows != 1 && b_rows != F8_GROUP)) return 0;
+  return partial_bytes(M, N, cut_of(M, N, K, groups, b_rows).ranges);
 }
 
 int moe_matmul_fp8(int64_t M, int64_t N, int64_t K, int64_t groups, const void* a_codes, int64_t lda,

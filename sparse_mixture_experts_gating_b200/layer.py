@@ -69,8 +69,8 @@ def _on(index: int, stream):
 
 
 @functools.lru_cache(maxsize=4096)
-def _matmul_workspace(M: int, N: int, K: int, G: int) -> int:
-    return int(lib().moe_matmul_fp8_workspace_bytes(M, N, K, G))
+def _matmul_workspace(M: int, N: int, K: int, G: int, b_rows: int) -> int:
+    return int(lib().moe_matmul_fp8_scratch_bytes(M, N, K, G, b_rows))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -447,7 +447,7 @@ def matmul_fp8(a, b, *, offsets: Optional[torch.Tensor] = None, out_dtype=torch.
     with _on(dev, stream) as handle:
         if out is None:
             out = sa.new_empty((M, N), dtype=out_dtype)
-        n = _matmul_workspace(M, N, K, G)
+        n = _matmul_workspace(M, N, K, G, b_rows)
         ws = sa.new_empty(n, dtype=torch.uint8) if n else None
         check(lib().moe_matmul_fp8(M, N, K, G, ac.data_ptr(), fa[3], sa.data_ptr(), bc.data_ptr(), fb[3], sb.data_ptr(),
                                b_rows, None if offsets is None else offsets.data_ptr(), out.data_ptr(), out_kind, ld_out,

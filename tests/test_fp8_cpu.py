@@ -282,3 +282,16 @@ def test_a_cut_of_few_rows_stays_within_one_wave(L):
                 assert n == (0 if ranges == 1 else 4 * M * N * ranges)
                 assert ranges == 1 or tiles * ranges <= 148, (groups, M, N)
                 assert ranges == 1 or tiles < 75, (groups, M, N)
+
+
+def test_product_scratch_is_what_the_call_writes(L):
+    """Up to eight rows with 128-row scales sum their few ranges in clusters, without
+    partials; with a scale a row, or with more rows, the partials need their room."""
+    both = L.moe_matmul_fp8_workspace_bytes
+    scratch = L.moe_matmul_fp8_scratch_bytes
+    for M, N, K in ((1, 14336, 4096), (8, 14336, 4096), (8, 768, 2048)):
+        assert scratch(M, N, K, 1, 128) == 0 and scratch(M, N, K, 1, 1) == both(M, N, K, 1) > 0
+    for M, N, K in ((9, 14336, 4096), (64, 768, 2048), (8, 32, 1 << 14), (300, 256, 8192)):
+        assert scratch(M, N, K, 1, 128) == scratch(M, N, K, 1, 1) == both(M, N, K, 1) > 0
+    for args in ((0, 1, 1, 1, 1), (1, 1, 1, 257, 128), (1, 256, 1 << 14, 1, 2), (1 << 62, 1, 1, 1, 1)):
+        assert scratch(*args) == 0

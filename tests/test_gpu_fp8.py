@@ -390,3 +390,31 @@ def test_binding_refusals():
     empty = matmul_fp8((a[0][:0], a[1][:0]), b)
     assert empty.shape == (0, 64)
     status()
+
+
+def test_a_product_summed_in_clusters_takes_no_workspace():
+    from sparse_mixture_experts_gating_b200._lib import MOE_ERR_INVALID_ARG, MOE_OK, lib
+    N, K = 768, 4096
+    a = quantize_fp8(torch.randn((16, K), device="cuda", generator=gen(72)))
+    w = torch.randn((N, K), device="cuda", generator=gen(73))
+    b, br = quantize_fp8(w, block_rows=128), quantize_fp8(w)
+
+    def call(M, pair, b_rows, ws, n):
+        out = torch.full((M, N), float("nan"), device="cuda")
+        rc = lib().moe_matmul_fp8(M, N, K, 1, a[0].data_ptr(), K, a[1].data_ptr(), pair[0].data_ptr(), K, pair[1].data_ptr(),
+                                  b_rows, None, out.data_ptr(), 0, N, ws, n, torch.cuda.current_stream().cuda_stream)
+        return rc, out
+
+    for M, pair, b_rows, clustered in ((1, b, 128, True), (8, b, 128, True), (8, br, 1, False), (16, b, 128, False)):
+        n = lib().moe_matmul_fp8_scratch_bytes(M, N, K, 1, b_rows)
+        assert (n == 0) == clustered and n <= lib().moe_matmul_fp8_workspace_bytes(M, N, K, 1)
+        rc, out = call(M, pair, b_rows, None, 0)
+        if clustered:
+            assert rc == MOE_OK
+        else:
+            assert rc == MOE_ERR_INVALID_ARG
+            ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+            rc, out = call(M, pair, b_rows, ws.data_ptr(), n)
+            assert rc == MOE_OK
+        status()
+        assert torch.equal(out, matmul_fp8((a[0][:M], a[1][:M]), pair, out_dtype=F32))
