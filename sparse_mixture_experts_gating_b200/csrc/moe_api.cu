@@ -45,6 +45,16 @@ int fail(int code, const std::string& msg) {
   return code;
 }
 
+// No C++ exception (a message that finds no memory) leaves a C entry.
+template <typename F>
+int guarded(const F& f) {
+  try {
+    return f();
+  } catch (...) {
+    return MOE_ERR_CUDA;
+  }
+}
+
 constexpr int kMaxDevices = 64;
 
 struct DeviceInfo {
@@ -956,8 +966,10 @@ int moe_forward(moe_handle h, int64_t T, const void* x, const float* W_r, const 
   ew.W1 = W1;
   ew.W3 = W3;
   ew.W2 = W2;
-  return forward_impl(h, T, x, W_r, b_r, ew, y, expert_counts, dropped, aux_loss, z_loss, workspace,
-                      workspace_bytes, dbg, stream, "moe_forward");
+  return guarded([&] {
+    return forward_impl(h, T, x, W_r, b_r, ew, y, expert_counts, dropped, aux_loss, z_loss, workspace,
+                        workspace_bytes, dbg, stream, "moe_forward");
+  });
 }
 
 size_t moe_workspace_bytes_w4(moe_handle h, int64_t T) {
@@ -979,8 +991,10 @@ int moe_forward_w4(moe_handle h, int64_t T, const void* x, const float* W_r, con
   ew.S1 = W1_scales;
   ew.S3 = W3_scales;
   ew.S2 = W2_scales;
-  return forward_impl(h, T, x, W_r, b_r, ew, y, expert_counts, dropped, aux_loss, z_loss, workspace,
-                      workspace_bytes, dbg, stream, "moe_forward_w4");
+  return guarded([&] {
+    return forward_impl(h, T, x, W_r, b_r, ew, y, expert_counts, dropped, aux_loss, z_loss, workspace,
+                        workspace_bytes, dbg, stream, "moe_forward_w4");
+  });
 }
 
 size_t moe_workspace_bytes_fp8(moe_handle h, int64_t T) {
@@ -1001,8 +1015,10 @@ int moe_forward_fp8(moe_handle h, int64_t T, const void* x, const float* W_r, co
   ew.S1 = W1_scales;
   ew.S3 = W3_scales;
   ew.S2 = W2_scales;
-  return forward_impl(h, T, x, W_r, b_r, ew, y, expert_counts, dropped, aux_loss, z_loss, workspace,
-                      workspace_bytes, dbg, stream, "moe_forward_fp8");
+  return guarded([&] {
+    return forward_impl(h, T, x, W_r, b_r, ew, y, expert_counts, dropped, aux_loss, z_loss, workspace,
+                        workspace_bytes, dbg, stream, "moe_forward_fp8");
+  });
 }
 
 int moe_quantize_int4(const void* W, int64_t rows, int64_t K, uint32_t* codes, void* scales, void* stream) {
@@ -1065,11 +1081,11 @@ size_t moe_backward_workspace_bytes(moe_handle h, int64_t T) {
   return make_bw_layout(*h, make_layout(*h, T)).total;
 }
 
-int moe_backward_logits(moe_handle h, int64_t T, const void* x, const float* W_r, const float* b_r, const void* W1,
-                        const void* W3, const void* W2, const void* dy, float aux_coef, float z_coef,
-                        const float* dlogits, float* dx, float* dW_r, float* db_r, float* dW1, float* dW3, float* dW2,
-                        const void* workspace, size_t workspace_bytes, void* bw_workspace, size_t bw_workspace_bytes,
-                        void* stream) {
+static int backward_impl(moe_handle h, int64_t T, const void* x, const float* W_r, const float* b_r, const void* W1,
+                         const void* W3, const void* W2, const void* dy, float aux_coef, float z_coef,
+                         const float* dlogits, float* dx, float* dW_r, float* db_r, float* dW1, float* dW3, float* dW2,
+                         const void* workspace, size_t workspace_bytes, void* bw_workspace, size_t bw_workspace_bytes,
+                         void* stream) {
   if (h == nullptr) return fail(MOE_ERR_INVALID_ARG, "moe_backward: handle is NULL");
   const moe_layer& L = *h;
   if (T < 0) return fail(MOE_ERR_INVALID_ARG, "moe_backward: T < 0");
@@ -1213,6 +1229,17 @@ int moe_backward_logits(moe_handle h, int64_t T, const void* x, const float* W_r
   if (ce != cudaSuccess) return fail(MOE_ERR_CUDA, std::string("moe_backward: ") + cudaGetErrorString(ce));
   t_err.clear();
   return MOE_OK;
+}
+
+int moe_backward_logits(moe_handle h, int64_t T, const void* x, const float* W_r, const float* b_r, const void* W1,
+                        const void* W3, const void* W2, const void* dy, float aux_coef, float z_coef,
+                        const float* dlogits, float* dx, float* dW_r, float* db_r, float* dW1, float* dW3, float* dW2,
+                        const void* workspace, size_t workspace_bytes, void* bw_workspace, size_t bw_workspace_bytes,
+                        void* stream) {
+  return guarded([&] {
+    return backward_impl(h, T, x, W_r, b_r, W1, W3, W2, dy, aux_coef, z_coef, dlogits, dx, dW_r, db_r, dW1, dW3, dW2,
+                         workspace, workspace_bytes, bw_workspace, bw_workspace_bytes, stream);
+  });
 }
 
 int moe_backward(moe_handle h, int64_t T, const void* x, const float* W_r, const float* b_r, const void* W1,

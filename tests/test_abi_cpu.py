@@ -284,3 +284,47 @@ def test_product_path_never_imports_the_oracle():
             if f.endswith((".py", ".cu", ".cuh", ".h", ".cpp")):
                 src = open(os.path.join(root, f), encoding="utf-8").read()
                 assert "import oracle" not in src and "from oracle" not in src, f
+
+
+NO_MEMORY = r"""
+#include <cstdlib>
+#include <new>
+static int none = 0;
+extern "C" void no_memory(int v) { none = v; }
+void* operator new(std::size_t n) {
+  if (none) throw std::bad_alloc();
+  return std::malloc(n ? n : 1);
+}
+void operator delete(void* p) noexcept { std::free(p); }
+void operator delete(void* p, std::size_t) noexcept { std::free(p); }
+"""
+CALLS = r"""
+import ctypes, sys
+heap, moe = ctypes.CDLL(None), ctypes.CDLL(sys.argv[1])
+codes = []
+for name, args in (("moe_forward", 17), ("moe_forward_w4", 20), ("moe_forward_fp8", 20), ("moe_backward", 22),
+                   ("moe_backward_logits", 23), ("moe_router_balance", 16), ("moe_router_balance_backward", 15),
+                   ("moe_quantize_fp8", 12), ("moe_matmul_fp8", 18)):
+    # (every argument 0: a NULL handle, or no rows and no columns; refused before anything is read)
+    f = getattr(moe, name)
+    heap.no_memory(1)
+    codes.append(f(*[ctypes.c_void_p(0)] * args))
+    heap.no_memory(0)
+    print(name, codes[-1], flush=True)
+"""
+
+
+def test_no_exception_leaves_a_c_entry(L, tmp_path):
+    """Each entry whose message finds no memory returns a code; the process lives on."""
+    import subprocess
+    import sys
+    (tmp_path / "heap.cpp").write_text(NO_MEMORY)
+    (tmp_path / "calls.py").write_text(CALLS)
+    so = str(tmp_path / "heap.so")
+    subprocess.run(["g++", "-shared", "-fPIC", "-O1", "-o", so, str(tmp_path / "heap.cpp")], check=True)
+    r = subprocess.run([sys.executable, str(tmp_path / "calls.py"), _lib.LIB_PATH], env=dict(os.environ, LD_PRELOAD=so),
+                       capture_output=True, text=True, timeout=120)
+    lines = dict(line.split() for line in r.stdout.splitlines())
+    assert r.returncode == 0 and len(lines) == 9, (r.stdout, r.stderr[-500:])
+    for name in ("moe_forward", "moe_forward_w4", "moe_forward_fp8", "moe_backward", "moe_backward_logits"):
+        assert int(lines[name]) == _lib.MOE_ERR_CUDA, lines  # a message too long for the string's own room
