@@ -401,7 +401,8 @@ MOE_API int moe_backward(moe_handle h, int64_t T, const void* x, const float* W_
 /*
  * moe_backward with a further gradient of the router logits: dlogits [T][E]
  * fp32 (NULL: none) is added to the one that the loss above gives them, before
- * it goes on to x, W_r and b_r.  moe_router_balance_backward makes one.
+ * it goes on to x, W_r and b_r; 4-byte aligned.  moe_router_balance_backward
+ * makes one.
  */
 MOE_API int moe_backward_logits(moe_handle h, int64_t T, const void* x, const float* W_r, const float* b_r,
                                 const void* W1, const void* W3, const void* W2, const void* dy, float aux_coef,

@@ -1125,6 +1125,8 @@ static int backward_impl(moe_handle h, int64_t T, const void* x, const float* W_
                        reinterpret_cast<uintptr_t>(dW3);
   if ((al & 15) != 0)
     return fail(MOE_ERR_INVALID_ARG, "moe_backward: x, dy, weights, dx and the expert-weight gradients must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(dlogits) & 3) != 0)
+    return fail(MOE_ERR_INVALID_ARG, "moe_backward: dlogits must be aligned to its elements");
   DeviceInfo* di = nullptr;
   cudaError_t de = device_info(&di);
   if (de != cudaSuccess) return fail(MOE_ERR_CUDA, std::string("moe_backward: ") + cudaGetErrorString(de));

@@ -295,3 +295,13 @@ def test_product_scratch_is_what_the_call_writes(L):
         assert scratch(M, N, K, 1, 128) == scratch(M, N, K, 1, 1) == both(M, N, K, 1) > 0
     for args in ((0, 1, 1, 1, 1), (1, 1, 1, 257, 128), (1, 256, 1 << 14, 1, 2), (1 << 62, 1, 1, 1, 1)):
         assert scratch(*args) == 0
+
+
+@pytest.mark.parametrize("act", [0, 1])
+def test_backward_refuses_a_logit_gradient_off_its_elements(L, act):
+    h = create(L, 8, 2, 64, 64, act, 1, 0.0, 1)
+    n, W3 = 1 << 40, P if act else None
+    for dl in (ODD, ctypes.c_void_p(4098)):
+        assert L.moe_backward_logits(h, 4, P, P, None, P, W3, P, P, 0.0, 0.0, dl, P, P, None, P, W3, P, P, n, P, n, None) == INVALID
+        assert b"dlogits" in L.moe_last_error()
+    L.moe_destroy(h)
