@@ -278,13 +278,19 @@ MOE_API int moe_forward_w4(moe_handle h, int64_t T, const void* x, const float* 
  * + 1]; NULL with one group: every row).  A [M][K] has block_rows 1; B
  * [groups][N][K] has block_rows b_rows = 128 (weights) or 1.  out is bf16 or
  * fp32, rows ld_out elements apart; rows of no group are left as they were.
- * Each block of 128 along K is summed on the tensor cores, the blocks in fp32
- * in order (the result does not depend on other rows or on timing), and the
- * sum is rounded once.  With the quantiser's transposed form these are the
- * three products of a linear layer y = x W^T:
+ * Each block of 128 along K is summed on the tensor cores and the blocks in
+ * fp32, in order; where few rows would leave SMs idle, K is cut into ranges
+ * of blocks, each summed by itself, and then the ranges are added, in order.
+ * The sum is rounded once.  M, N, K, groups and b_rows alone choose the cut:
+ * for the same ones a row has the same bits whatever the other rows hold and
+ * wherever the groups begin; for another M its last bits may differ (any
+ * order is within fp32's bound for sums of K terms).  With the quantiser's
+ * transposed form these are the three products of a linear layer y = x W^T:
  *     y  = (x block_rows 1) (W block_rows 128)
  *     dx = (dy block_rows 1) (W transposed, block_rows 128)
  *     dW = (dy transposed, block_rows 1) (x transposed, block_rows 1), b_rows 1
+ * (Groups are rows of A: y and dx of experts are one call each, dW of experts
+ * is one call an expert, on that expert's rows.)
  *   Codes 16-byte aligned, lda and ldb multiples of 16; scales contiguous and
  *   4-byte aligned; 1 <= groups <= 256; M may be 0, N and K at least 1.  The
  *   product of two scales must be a normal fp32 number.  Offsets outside [0,

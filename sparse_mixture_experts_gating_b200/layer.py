@@ -412,7 +412,10 @@ def matmul_fp8(a, b, *, offsets: Optional[torch.Tensor] = None, out_dtype=torch.
     quantize_fp8: a with block_rows 1, b with 128 or 1.  With offsets (int32
     [G + 1] on the device, ascending) b is [G, N, K] and rows offsets[g] ..
     offsets[g + 1] - 1 of a are multiplied by b[g]; rows of no group are left as
-    they were in ``out``.  Returns [M, N] in out_dtype (bf16 or fp32)."""
+    they were in ``out``.  Returns [M, N] in out_dtype (bf16 or fp32).  The same
+    sizes give a row the same bits whatever stands beside it; other batch sizes
+    may cut K elsewhere and change the last ones.  The product of two scales
+    must be a normal fp32 number."""
     (ac, sa), (bc, sb) = a, b
     dev = _device_of("a codes", ac)
     out_kind = DTYPE.get(out_dtype)

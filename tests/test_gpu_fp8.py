@@ -418,3 +418,32 @@ def test_a_product_summed_in_clusters_takes_no_workspace():
             assert rc == MOE_OK
         status()
         assert torch.equal(out, matmul_fp8((a[0][:M], a[1][:M]), pair, out_dtype=F32))
+
+
+@pytest.mark.parametrize("groups", [0, 3])
+def test_a_row_beside_other_rows_and_in_batches_of_other_sizes(groups):
+    """The sizes choose how K is cut: among calls of the same sizes a row has the
+    same bits whatever stands beside it; among others it stays within the bound."""
+    N, K, most = 1024, 4096, 512
+    g = gen(71)
+    a = quantize_fp8(torch.randn((most, K), device="cuda", generator=g))
+    b = quantize_fp8(torch.randn(((groups,) if groups else ()) + (N, K), device="cuda", generator=g), block_rows=128)
+    other = quantize_fp8(torch.randn((most, K), device="cuda", generator=g))
+    av = F.values(code_values(a[0]), a[1].cpu().numpy(), 1)[:1]
+    b0 = (b[0][0], b[1][0]) if groups else b
+    bv = F.values(code_values(b0[0]), b0[1].cpu().numpy(), 128)
+    exact, bound = av @ bv.T, F.product_bound(av, bv)
+    for M in (1, 8, 16, 64, 65, 128, 129, 256, 512):
+        # (groups: the row is the first group's first, the others share what is left)
+        off = torch.tensor([0, (M + 1) // 2, M, M], dtype=torch.int32, device="cuda") if groups else None
+        mixed = tuple(torch.cat([p[:1].view(torch.uint8), o[1:M].view(torch.uint8)]).view(p.dtype).view(M, -1)
+                      for p, o in zip(a, other))
+        y = matmul_fp8((a[0][:M], a[1][:M]), b, offsets=off, out_dtype=F32)
+        z = matmul_fp8(mixed, b, offsets=off, out_dtype=F32)
+        status()
+        assert torch.equal(y[0], z[0]), M
+        if M >= 8:  # the row elsewhere, the groups begun elsewhere
+            moved = tuple(torch.roll(p[:M].view(torch.uint8), 3, 0).view(p.dtype) for p in a)
+            off3 = torch.tensor([3, M - 2, M - 2, M], dtype=torch.int32, device="cuda") if groups else None
+            assert torch.equal(y[0], matmul_fp8(moved, b, offsets=off3, out_dtype=F32)[3]), M
+        assert (np.abs(y[:1].double().cpu().numpy() - exact) <= bound).all(), M
