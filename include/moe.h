@@ -90,7 +90,9 @@ enum {
  *   drop_mask   [T][k] uint8      : 1 if assignment (t, j) was dropped
  *   expert_offsets [E+1] int32    : first row of each expert in the sorted buffer
  *   y_f32       [T][d] fp32, write: the output in fp32, before its final rounding to
- *                                   the layer dtype (y is its round-to-nearest-even image)
+ *                                   the layer dtype (y is its round-to-nearest-even image);
+ *                                   of moe_forward_fp8: the fp32 sum of addends that may be
+ *                                   fp16 (moe_set_hidden_precision)
  *   events[2*s], events[2*s+1]    : cudaEvent_t recorded on the stream right before
  *                                   and after the launches of stage s (MOE_STAGE_*)
  */
@@ -143,6 +145,11 @@ MOE_API int moe_create(int num_experts, int k, int d, int d_ff, int act, int gat
  *     1e-2 * RMS) and a mean relative error of about 1.6e-3 before the final
  *     cast, which the cast to bf16 raises to about 2.3e-3 in the returned y
  *     (the bar is 2e-3).  Use it only where that is acceptable.
+ * moe_forward_fp8 holds the hidden activation in its own 8-bit form; there the
+ * modes differ in the expert outputs that the combine adds: with
+ * MOE_HIDDEN_BF16X2 they lie in fp32, with the others in fp16 (11 significant
+ * bits) times a power of two for each 128 columns, where the batch has over 64
+ * tokens and the second projection's K is not cut.
  * Changes moe_workspace_bytes() (MOE_HIDDEN_F16 and the automatic mode at
  * large batches add the W2 image: (E + n_shared) * d * d_ff * 2 bytes).
  * fp32 layers ignore it.  Returns MOE_OK or MOE_ERR_INVALID_ARG.
@@ -305,7 +312,9 @@ MOE_API int moe_forward_w4(moe_handle h, int64_t T, const void* x, const float* 
  * reads x itself; the experts read x and the hidden activation quantised with
  * block_rows 1.  Arguments, results and errors as moe_forward; W3_codes and
  * W3_scales are NULL for ReLU layers; the workspace is
- * moe_workspace_bytes_fp8(h, T) bytes.  A NaN of the first projection stays one
+ * moe_workspace_bytes_fp8(h, T) bytes.  Over 64 tokens the gated outputs of the
+ * experts may be rounded to fp16 before they are added
+ * (moe_set_hidden_precision).  A NaN of the first projection stays one
  * under both activations (ReLU in moe_forward and moe_forward_w4 gives 0).  moe_backward does not serve layers run
  * this way.
  */

@@ -94,7 +94,8 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 // The second projection splits its K range for at most this many tiles.
 constexpr int kSplitMaxTiles = 4 * kSplitTargetCtas;
 
-// (4-bit and 8-bit weights always go through the fp32 rows and the combine.)
+// (4-bit and 8-bit weights always go through the combine, from fp32 rows or,
+// large 8-bit batches, scaled fp16 ones.)
 enum Weights { W_NATIVE = 0, W_INT4 = 1, W_FP8 = 2 };
 
 bool need_yp_of(const moe_layer& L, Weights kind) {
@@ -208,8 +209,8 @@ SmallSplits small_splits_of(const moe_layer& L, int64_t T) {
 
 // kind W_INT4: the layout of moe_forward_w4 (4-bit weights: hidden as a hi + lo
 // pair, fp32 rows for the combine, no fp16 image of W2); W_FP8: that of
-// moe_forward_fp8 (x and the hidden activation as codes with scales, fp32 rows
-// for the combine).
+// moe_forward_fp8 (x and the hidden activation as codes with scales, fp32 or
+// scaled fp16 rows for the combine).
 Layout make_layout(const moe_layer& L, int64_t T, Weights kind = W_NATIVE) {
   const bool w4 = kind == W_INT4, fp8 = kind == W_FP8;
   Layout w;
@@ -748,11 +749,12 @@ int forward_impl(moe_handle h, int64_t T, const void* x, const float* W_r, const
     a2.split_stride = static_cast<int64_t>(w.s_max) * L.d;
     a2.row_gate = r.row_gate;
     // Batches of over 64 tokens whose K is not cut: the gated rows in fp16 with
-    // a power of two for each 128 columns.  That rounds each to 12 bits (half a
-    // unit 2^-12, against y's own 2^-9), and halves the bytes that lie between
+    // a power of two for each 128 columns.  That rounds each to 11 bits (half a
+    // unit 2^-11, against y's own 2^-8), and halves the bytes that lie between
     // the second projection and the combine, which bind both where d_ff is
     // small (16384 tokens, 128 experts of d_ff 768, top-4: 724 -> 616 us).
-    h16 = T > 64 && w.ksplit == 1;
+    // MOE_HIDDEN_BF16X2 keeps them in fp32.
+    h16 = T > 64 && w.ksplit == 1 && L.hidden != MOE_HIDDEN_BF16X2;
     if (h16) {
       a2.epi = FP8_GATE_H16;
       a2.out_scales = reinterpret_cast<float*>(ws + w.Yp + align256(sizeof(uint16_t) * static_cast<size_t>(w.s_max) * L.d));

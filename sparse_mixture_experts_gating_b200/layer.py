@@ -127,7 +127,9 @@ class MoELayer:
     hidden (bf16 layers): "auto" (default) holds the hidden activation in fp16
     for batches of at least 1024 rows per expert and as a hi + lo pair of
     bf16 planes otherwise; "f16" and "bf16x2" force one of those; "bf16" is
-    one bf16 plane (outside the parity bar; see include/moe.h).
+    one bf16 plane (outside the parity bar; see include/moe.h).  forward_fp8
+    of over 64 tokens may round the experts' gated outputs to fp16 before it
+    adds them; with "bf16x2" they stay in fp32.
     n_shared: shared experts every token visits; W1, W3, W2 then hold
     num_experts + n_shared experts, the shared ones last.
     """

@@ -305,3 +305,23 @@ def test_backward_after_an_8_bit_forward():
     status()
     for name, g in want.items():
         assert g is None or (torch.equal(g, kept[name]) and torch.equal(g, again[name])), name
+
+
+@pytest.mark.parametrize("T", [65, 700])
+def test_hidden_precision_keeps_the_gated_rows_in_fp32(T):
+    """Over 64 tokens whose second projection's K is not cut: the gated rows are
+    rounded to fp16 (11 bits) unless MOE_HIDDEN_BF16X2 asks for fp32."""
+    w = Workload("gated_rows", T=T, d=256, E=1, k=1, d_ff=128, act=R, gate=RN, capacity_factor=0.0, dtype=DTYPE_BF16,
+                 dyadic=True, seed=64)
+    inp = make_inputs(w, device="cuda")
+    q = quantized(inp)
+    y16, y32 = (run(w, inp, q, layer_for(w, hidden))["y_f32"] for hidden in ("auto", "bf16x2"))
+    assert not (y16.view(np.uint32) & 0x1FFF).any()            # one row of gate 1: 11 bits of 24
+    assert ((y32.view(np.uint32) & 0x1FFF) != 0).mean() > 0.9  # all of them
+    # half a unit of 11 bits, or of the smallest number of rows whose largest is at least 2^14
+    top = np.abs(y32).reshape(T, -1, 128).max(2).repeat(128, 1)
+    assert (np.abs(y16.astype(np.float64) - y32) <= np.abs(y32) * 2.0 ** -11 + top * 2.0 ** -39).all()
+    w = CASES[4]  # and against the definition
+    inp = make_inputs(w, device="cuda")
+    q = quantized(inp)
+    check(w, inp, q, run(w, inp, q, layer_for(w, "bf16x2")))
