@@ -442,7 +442,10 @@ MOE_API int moe_backward_logits(moe_handle h, int64_t T, const void* x, const fl
  *   tokens [sequences] int32: n_b
  * An expert whose logit is -inf is never chosen and has p = 0; a token with no
  * expert left counts as padding.  A sequence without tokens has aux = z = 0.
- * Other non-finite logits make the results NaN.
+ * A NaN makes its sequence's aux and z NaN, and so does +inf, but for aux with
+ * MOE_SCORE_SIGMOID, where it is a score of 1; either makes its token's
+ * gradient NaN.  Other sequences see nothing of it, the other tokens of its
+ * own the counts alone, in which a token with a NaN has at most k choices.
  *
  * moe_router_balance_backward: dlogits [T][E] fp32, the gradient of sum_b daux_b
  * aux_b + dz_b z_b (daux, dz [sequences] fp32; NULL: 0), the counts held

@@ -305,3 +305,59 @@ def test_binding_refusals():
             router_balance(l, k)
     d = router_balance_backward(l, c, t, None, None, 2)
     assert not d.any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_infinite_logits_mark_their_sequence_alone(scoring, dtype):
+    """A logit of +inf: z is NaN; aux too where scores are a softmax, while its sigmoid
+    is a score of 1.  The other sequences and the other tokens' gradients keep their values."""
+    cuts, k = [0, 40, 90, 130], 2
+    l, _ = make(130, 24, 8, dtype, False, False)
+    off = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+    one = torch.ones(3, device="cuda")
+    clean = run(l, k, off, None, scoring, one, one)
+    t, e = 57, 5
+    far = l.clone()
+    far[t, e] = float("inf")
+    aux, z, counts, tokens, d = run(far, k, off, None, scoring, one, one)
+    status()
+    for i in (0, 2):
+        assert aux[i] == clean[0][i] and z[i] == clean[1][i] and torch.equal(counts[i], clean[2][i])
+    assert torch.isnan(z[1]) and torch.equal(tokens, clean[3])
+    assert torch.isnan(d[t]).all()
+    keep = torch.ones(130, dtype=torch.bool, device="cuda")
+    keep[cuts[1]:cuts[2]] = False
+    assert torch.equal(d[keep], clean[4][keep])
+    keep[cuts[1]:cuts[2]] = True
+    keep[t] = False
+    assert torch.isfinite(d[keep]).all()
+    if scoring == "softmax":
+        assert torch.isnan(aux[1])
+    else:  # the token's score of that expert is that of a logit past fp32's resolution
+        far[t, e] = 100.0
+        ra, _, rc, _ = D.loss(far.double().cpu().numpy(), k, cuts, None, scoring)
+        assert torch.equal(counts.cpu(), torch.from_numpy(rc).to(torch.int32))
+        assert abs(aux[1].item() - ra[1]) <= 300 * D.ULP * ra[1]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_nan_logits_mark_their_sequence_alone(scoring, dtype):
+    cuts, k = [0, 40, 90, 130], 3
+    l, _ = make(130, 24, 9, dtype, False, False)
+    off = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+    one = torch.ones(3, device="cuda")
+    clean = run(l, k, off, None, scoring, one, one)
+    for e in (slice(5, 6), slice(0, 24)):  # one of the token's logits, and all
+        for sign in (1.0, -1.0):
+            bad = l.clone()
+            bad[57, e] = torch.tensor(float("nan"), device="cuda").copysign(torch.tensor(sign, device="cuda")).to(dtype)
+            aux, z, counts, tokens, d = run(bad, k, off, None, scoring, one, one)
+            status()
+            for i in (0, 2):
+                assert aux[i] == clean[0][i] and z[i] == clean[1][i] and torch.equal(counts[i], clean[2][i])
+            assert torch.isnan(aux[1]) and torch.isnan(z[1]) and torch.isnan(d[57]).all()
+            assert 50 * k - k <= counts[1].sum().item() <= 50 * k and torch.equal(tokens, clean[3])
+            assert torch.equal(d[:40], clean[4][:40]) and torch.equal(d[90:], clean[4][90:])
+            assert torch.isfinite(torch.cat([d[40:57], d[58:90]])).all()
