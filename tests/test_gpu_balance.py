@@ -361,3 +361,38 @@ def test_nan_logits_mark_their_sequence_alone(scoring, dtype):
             assert 50 * k - k <= counts[1].sum().item() <= 50 * k and torch.equal(tokens, clean[3])
             assert torch.equal(d[:40], clean[4][:40]) and torch.equal(d[90:], clean[4][90:])
             assert torch.isfinite(torch.cat([d[40:57], d[58:90]])).all()
+
+
+def test_offsets_out_of_order_write_every_result_and_nothing_beside_them():
+    """The C entries with every output and the workspace between guards: offsets that
+    leave [0, T] or do not ascend write no byte outside, and a gradient for every token."""
+    from sparse_mixture_experts_gating_b200._lib import MOE_OK, lib
+    T, E, k, B, G = 500, 12, 3, 3, 4096
+    l, _ = make(T, E, 6, F32, False, False)
+    one = torch.ones(B, device="cuda")
+    sane = torch.tensor([0, 150, 320, T], dtype=torch.int32, device="cuda")
+    _, _, c0, t0, _ = run(l, k, sane, None, "softmax", one, one)
+    n = lib().moe_router_balance_workspace_bytes(T, E, B)
+    sizes = dict(aux=4 * B, z=4 * B, counts=4 * B * E, tokens=4 * B, ws=n, d=4 * T * E)
+    room = {name: torch.full((G + (size + 15) // 16 * 16 + G,), 0xA5, dtype=torch.uint8, device="cuda")
+            for name, size in sizes.items()}
+    p = {name: t.data_ptr() + G for name, t in room.items()}
+    s = torch.cuda.current_stream().cuda_stream
+    for cuts in ([-5, 100, 50, 900], [400, 300, 200, 100], [0, 2 ** 31 - 1, -2 ** 31, 500], [500, 500, 500, 0],
+                 [-2 ** 31, -1, 2 ** 31 - 1, 2 ** 31 - 1], [7, 7, 500, 501]):
+        for t in room.values():
+            t.fill_(0xA5)
+        off = torch.tensor(cuts, dtype=torch.int64).to(torch.int32).cuda()
+        assert lib().moe_router_balance(T, E, k, l.data_ptr(), 0, 0, B, off.data_ptr(), None, p["aux"], p["z"], p["counts"],
+                                        p["tokens"], p["ws"], n, s) == MOE_OK
+        assert lib().moe_router_balance_backward(T, E, k, l.data_ptr(), 0, 0, B, off.data_ptr(), None, c0.data_ptr(),
+                                                 t0.data_ptr(), one.data_ptr(), one.data_ptr(), p["d"], s) == MOE_OK
+        status()
+        for name, size in sizes.items():
+            t = room[name]
+            assert (t[:G] == 0xA5).all() and (t[G + size:] == 0xA5).all(), (name, cuts)
+        d = room["d"][G:G + sizes["d"]].view(F32)
+        assert torch.isfinite(d).all() and not (d == torch.full((4,), 0xA5, dtype=torch.uint8).view(F32).item()).any(), cuts
+        for name in ("aux", "z", "counts", "tokens"):  # (whatever they say, they are written)
+            words = room[name][G:G + sizes[name]].view(torch.int32)
+            assert not (words == torch.full((4,), 0xA5, dtype=torch.uint8).view(torch.int32).item()).any(), (name, cuts)
