@@ -325,3 +325,26 @@ def test_hidden_precision_keeps_the_gated_rows_in_fp32(T):
     inp = make_inputs(w, device="cuda")
     q = quantized(inp)
     check(w, inp, q, run(w, inp, q, layer_for(w, "bf16x2")))
+
+
+TILES = [  # more than two whole 128-row tiles a CTA: each epilogue's shared memory is written again under its stores
+    Workload("swiglu_tiles", T=4096, d=128, E=2, k=1, d_ff=1280, act=S, gate=SW, capacity_factor=0.0, dtype=DTYPE_BF16,
+             dyadic=True, seed=61),
+    Workload("relu_tiles", T=5120, d=128, E=2, k=1, d_ff=2048, act=R, gate=SW, capacity_factor=0.0, dtype=DTYPE_BF16,
+             dyadic=True, seed=62),
+    Workload("fp16_row_tiles", T=5120, d=2048, E=2, k=1, d_ff=128, act=R, gate=SW, capacity_factor=0.0,
+             dtype=DTYPE_BF16, dyadic=True, seed=63),
+]
+
+
+@pytest.mark.parametrize("w", TILES, ids=lambda w: w.name)
+def test_many_whole_tiles_a_cta(w):
+    inp = make_inputs(w, device="cuda")
+    q = quantized(inp)
+    layer = layer_for(w)
+    g = run(w, inp, q, layer)
+    check(w, inp, q, g)
+    for _ in range(8):
+        y, *_ = layer.forward_fp8(inp["x"], inp["W_r"], inp["b_r"], q["W1"], q["W3"], q["W2"])
+        assert torch.equal(y, g["y_dev"])
+    status()
