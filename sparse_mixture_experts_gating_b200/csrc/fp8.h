@@ -67,7 +67,7 @@ struct Fp8Args {
 };
 
 struct Fp8Params {
-  int G, N, K, bn, n_tiles, num_kb, ksplit, kb_per, cluster;
+  int G, N, n_tiles, num_kb, ksplit, kb_per, cluster;
   int64_t a_rows;
   const float* sa;
   int64_t sa_ld;

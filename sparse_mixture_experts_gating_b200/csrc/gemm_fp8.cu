@@ -1009,9 +1009,8 @@ cudaError_t plan_fp8(const Fp8Args& g, Fp8Plan* pl, const char** why) {
   Fp8Params& p = pl->p;
   p.G = g.G;
   p.N = g.N;
-  p.K = g.K;
-  p.bn = pair ? 128 : 256;
-  p.n_tiles = (g.N + p.bn - 1) / p.bn;
+  const int bn = pair ? 128 : 256;
+  p.n_tiles = (g.N + bn - 1) / bn;
   p.num_kb = (g.K + BK - 1) / BK;
   p.ksplit = g.epi == FP8_F32 || g.epi == FP8_PAIR_F32 ? std::max(1, std::min(g.ksplit, p.num_kb)) : 1;
   p.cluster = std::max(1, g.cluster);

@@ -23,7 +23,7 @@ struct RoutingArgs {
   const void* x;
   const void* x_rows;  // the rows the dispatch copies: x, or its 8-bit image (codes and scales)
   int d_rows;          // elements (of x's type) in one of them
-  int after_own;     // the launch before is the quantiser of the same call, which the router does not read
+  int after_own;     // the launch before is the quantiser of the same call, which the router does not read (bf16 x)
   const float* W_r;
   const float* b_r;
   const float* logits_in;

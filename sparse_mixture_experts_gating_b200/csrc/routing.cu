@@ -1163,14 +1163,13 @@ cudaError_t launch_route_small(const RoutingArgs& a, void* partials, cudaStream_
   const size_t smem = static_cast<size_t>(a.T) * a.E * sizeof(float);
   cudaError_t e;
   if (a.logits_in == nullptr) {  // the first kernel of the forward: an ordinary launch
-    if (a.after_own)  // ... or the second, beside the first, whose own wait has seen to x
-      e = a.x_is_bf16 ? launch_pdl(route_small_dot_kernel<__nv_bfloat16>, dim3(n_ds, a.E), dim3(256), 0, s, a, chunk, part)
-                      : launch_pdl(route_small_dot_kernel<float>, dim3(n_ds, a.E), dim3(256), 0, s, a, chunk, part);
-    else if (a.x_is_bf16)
-      route_small_dot_kernel<__nv_bfloat16><<<dim3(n_ds, a.E), 256, 0, s>>>(a, chunk, part);
-    else
-      route_small_dot_kernel<float><<<dim3(n_ds, a.E), 256, 0, s>>>(a, chunk, part);
-    if (!a.after_own) {
+    if (a.after_own) {  // ... or (bf16) the second, beside the first, whose own wait has seen to x
+      e = launch_pdl(route_small_dot_kernel<__nv_bfloat16>, dim3(n_ds, a.E), dim3(256), 0, s, a, chunk, part);
+    } else {
+      if (a.x_is_bf16)
+        route_small_dot_kernel<__nv_bfloat16><<<dim3(n_ds, a.E), 256, 0, s>>>(a, chunk, part);
+      else
+        route_small_dot_kernel<float><<<dim3(n_ds, a.E), 256, 0, s>>>(a, chunk, part);
       count_launch();
       e = cudaGetLastError();
     }
