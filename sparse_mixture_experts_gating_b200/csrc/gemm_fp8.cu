@@ -10,8 +10,11 @@
 // multiply by sa * sb and add it to fp32 registers while the next k-block's
 // MMAs fill the other accumulator.  Tiles are 128 rows x 256 columns.
 //
-// What bounds it: alone, a k-block's MMAs take 514 cycles, its 32768 additions 256
-// (the fp32 rate of an SM) and its read-back 144.  Together a k-block takes 930:
+// What bounds it, by form:
+//
+// Many rows, scales of 128 x 128 weights: alone, a k-block's MMAs take 514 cycles,
+// its 32768 additions 256 (the fp32 rate of an SM) and its read-back 144.  Together
+// a k-block takes 930:
 // the MMAs 720, the summing warps 730 and a wait of 200, for the read-back shares
 // TMEM with the accumulation (counters: tensor pipe 54 % active, shared memory's
 // banks 20 % reads and 20 % writes).  8192 x 14336 x 4096: 456 us in bursts (2.1
@@ -20,6 +23,15 @@
 // of 128 columns with 232 registers each were the fastest of the forms tried;
 // sixteen of 64 columns, MMAs of half the width with four accumulators, and
 // sums kept in register pairs took 1.1 to 1.4 times as long.
+// A scale for every column (SB1): each summing warp reads 128 column scales and
+// multiplies by them as well, 1.5 times as long (4736 x 4096 x 4096: 114 and 76.5 us).
+// Few k-blocks a tile: the epilogue, about 5 k-blocks long, is not hidden (128
+// ragged groups, 40961 x 768 x 2048: 95 us in bursts, eight tiles of 16 k-blocks a
+// CTA, of whose rows a sixth belong to no group).
+// A few rows: a k-block still costs its whole loop, 0.42 us with weights in L2 and
+// few CTAs, and HBM serves about 90 CTAs at that pace; the launch, the first loads
+// and the cluster's meeting are 5 us (one token times 14336 x 4096: 15.3 us, 12.2 with
+// the weights in L2).
 //
 // Warp roles (384 threads, one CTA per SM):
 //   warp 0       TMA producer
@@ -940,9 +952,9 @@ int fp8_ksplit(int64_t rows, int G, int N, int K, bool summed_anyway) {
   while (r2 < rows) r2 <<= 1;
   if (r2 <= 64) {
     // A few rows: the weights' stream is the time, and about 96 CTAs carry what
-    // HBM gives (a k-block takes a CTA 0.45 us, 73 GB/s).  One token times 14336 x
-    // 4096, 56 tiles: uncut 19.8 us, cut in two 18.2 us, in five 20.7 us, each
-    // with the second launch; 224 tiles, two experts' first projections: uncut 52
+    // HBM gives (a k-block takes a CTA's loop 0.42 to 0.45 us, 73 GB/s, wherever the
+    // weights lie).  One token times 14336 x 4096, 56 tiles: uncut 19.8 us, cut in
+    // two 18.2 us, in five 20.7 us, each with the second launch; 224 tiles, two experts' first projections: uncut 52
     // us, cut in three 57 us.  The ranges stay within one wave of CTAs: 86 tiles
     // (one token times 22016 x 4096) cut in two, 172 ranges, take 27.4 us, uncut 20.7.
     // Where a launch that follows sums the partials anyway, a cut is free, and
