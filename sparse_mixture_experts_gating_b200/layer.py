@@ -256,6 +256,14 @@ class MoELayer:
                 raise ValueError(f"forward_fp8: {name} is a (codes, scales) pair")
         if out is not None:
             _check_tensor("out", out, dev, torch.bfloat16, (T, self.d))
+        if stats is not None:
+            for name, t, dtype, n in zip(("expert_counts", "dropped", "aux_loss", "z_loss"), stats,
+                                         (torch.int32, torch.int32, torch.float32, torch.float32), (self.E, 1, 1, 1)):
+                _check_tensor(name, t, dev, dtype, (n,))
+        if workspace is not None:
+            _check_tensor("workspace", workspace, dev, torch.uint8)
+        if debug is not None:
+            self._check_debug(debug, T, dev)
         with _on(dev, stream) as handle:
             y = out if out is not None else torch.empty_like(x)
             if stats is None:
@@ -321,19 +329,32 @@ class MoELayer:
         check(lib().moe_balance_losses(self._h, T, _ptr(ws), _ptr(out), _stream_handle(stream)))
         return out
 
-    def debug_buffers(self, T: int, device) -> dict:
-        """Device tensors for every output field of moe_debug."""
+    def _debug_form(self, T: int) -> dict:
+        """Shape and dtype of every output field of moe_debug."""
         E, k = self.E, self.k
         return {
-            "logits_out": torch.empty((T, E), dtype=torch.float32, device=device),
-            "lse_out": torch.empty(T, dtype=torch.float32, device=device),
-            "topk_idx": torch.empty((T, k), dtype=torch.int32, device=device),
-            "topk_gate": torch.empty((T, k), dtype=torch.float32, device=device),
-            "dest_row": torch.empty((T, k), dtype=torch.int32, device=device),
-            "drop_mask": torch.empty((T, k), dtype=torch.uint8, device=device),
-            "expert_offsets": torch.empty(E + 1, dtype=torch.int32, device=device),
-            "y_f32": torch.empty((T, self.d), dtype=torch.float32, device=device),
+            "logits_out": ((T, E), torch.float32),
+            "lse_out": ((T,), torch.float32),
+            "topk_idx": ((T, k), torch.int32),
+            "topk_gate": ((T, k), torch.float32),
+            "dest_row": ((T, k), torch.int32),
+            "drop_mask": ((T, k), torch.uint8),
+            "expert_offsets": ((E + 1,), torch.int32),
+            "y_f32": ((T, self.d), torch.float32),
         }
+
+    def _check_debug(self, debug: dict, T: int, index: int) -> None:
+        form = dict(self._debug_form(T), logits_in=((T, self.E), torch.float32))
+        for name, t in debug.items():
+            if name not in form:
+                raise ValueError(f"debug: no field {name}")
+            if t is not None:
+                _check_tensor(name, t, index, form[name][1], form[name][0])
+
+    def debug_buffers(self, T: int, device) -> dict:
+        """Device tensors for every output field of moe_debug."""
+        return {name: torch.empty(shape, dtype=dtype, device=device)
+                for name, (shape, dtype) in self._debug_form(T).items()}
 
 
 def quantize_int4(W: torch.Tensor, stream=None):

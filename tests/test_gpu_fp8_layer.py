@@ -348,3 +348,40 @@ def test_many_whole_tiles_a_cta(w):
         y, *_ = layer.forward_fp8(inp["x"], inp["W_r"], inp["b_r"], q["W1"], q["W3"], q["W2"])
         assert torch.equal(y, g["y_dev"])
     status()
+
+
+def test_refusals_of_results_and_workspaces_of_the_wrong_form():
+    """What the kernels write through is checked like what they read."""
+    w = CASES[1]
+    inp = make_inputs(w, device="cuda")
+    q = quantized(inp)
+    layer = layer_for(w)
+    i32, f32 = torch.int32, torch.float32
+
+    def call(**kw):
+        return layer.forward_fp8(inp["x"], inp["W_r"], inp["b_r"], q["W1"], q["W3"], q["W2"], **kw)
+
+    def stats(n=w.E, counts=i32, losses=f32, device="cuda"):
+        return tuple(torch.zeros(m, dtype=t, device=device) for m, t in ((n, counts), (1, i32), (1, losses), (1, f32)))
+
+    dbg = layer.debug_buffers(w.T, "cuda")
+    n = layer.workspace_bytes_fp8(w.T)
+    for kw in (dict(stats=stats(n=w.E - 1)), dict(stats=stats(counts=torch.int64)), dict(stats=stats(losses=torch.float64)),
+               dict(stats=stats(device="cpu")), dict(workspace=torch.empty(n, dtype=torch.uint8)),
+               dict(workspace=torch.empty(n, dtype=torch.float32, device="cuda")),
+               dict(workspace=torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2]),
+               dict(debug=dict(dbg, y_f32=dbg["y_f32"][1:])), dict(debug=dict(dbg, topk_idx=dbg["topk_idx"].long())),
+               dict(debug=dict(dbg, lse_out=dbg["lse_out"].cpu())), dict(debug=dict(logits=dbg["logits_out"]))):
+        with pytest.raises(ValueError):
+            call(**kw)
+    with pytest.raises(MoEError):  # too small
+        call(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    given = stats()
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    got = call(stats=given, workspace=ws, debug=dict(dbg, drop_mask=None))
+    assert all(a is b for a, b in zip(got[1:], given))
+    for a, b in zip(got, call()):
+        assert torch.equal(a, b)
+    again = call(debug=dict(logits_in=dbg["logits_out"]))  # its own logits handed in
+    assert torch.equal(again[0], got[0])
+    status()
