@@ -14,11 +14,10 @@
 //
 // Many rows, scales of 128 x 128 weights: alone, a k-block's MMAs take 514 cycles,
 // its 32768 additions 256 (the fp32 rate of an SM) and its read-back 144.  Together
-// a k-block takes 930:
-// the MMAs 720, the summing warps 730 and a wait of 200, for the read-back shares
-// TMEM with the accumulation (counters: tensor pipe 54 % active, shared memory's
-// banks 20 % reads and 20 % writes).  8192 x 14336 x 4096: 456 us in bursts (2.1
-// PFLOP/s), 507-541 us back to back, where the board's power limit sets the
+// a k-block takes 930: the MMAs 720, the summing warps 730 and a wait of 200, for
+// the read-back shares TMEM with the accumulation (counters: tensor pipe 54 %
+// active, shared memory's banks 20 % reads and 20 % writes).  8192 x 14336 x 4096: 456 us in bursts (2.1
+// PFLOP/s), 507-542 us back to back, where the board's power limit sets the
 // clock (cuBLAS with one scale per tensor: 331 and 385 us).  Eight summing warps
 // of 128 columns with 232 registers each were the fastest of the forms tried;
 // sixteen of 64 columns, MMAs of half the width with four accumulators, and
@@ -314,7 +313,9 @@ __device__ __forceinline__ void add32(float* acc, const uint32_t (&t)[32], float
 }
 
 // silu(a) * b from the special function unit's exponential and reciprocal (each
-// good to two units; 0 once e^-a overflows, the limit of silu, whatever a b is).
+// good to two units, and the exponential's argument, rounded, moves it by up to
+// |a| units more: codes have 4 bits of the 24; 0 once e^-a overflows, the limit of
+// silu, whatever a b is).
 __device__ __forceinline__ float silu_mul(float a, float b) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a * -1.4426950408889634f));
