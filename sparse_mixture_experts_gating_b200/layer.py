@@ -103,6 +103,14 @@ def _check_tensor(name, t, index, dtype, shape=None, contiguous=True):
     raise ValueError(f"{name}: want a contiguous tensor")
 
 
+def _check_room(name, t, index, nbytes):
+    """A contiguous tensor on CUDA device ``index`` of at least ``nbytes`` bytes, whatever its type."""
+    if _device_of(name, t) != index:
+        raise ValueError(f"{name}: want a tensor on cuda:{index}, got {t.device}")
+    if not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
+        raise ValueError(f"{name}: want a contiguous tensor of {nbytes} bytes, got {t.dtype} {tuple(t.shape)}")
+
+
 def _debug_struct(debug: Optional[dict], events, stream) -> Optional[MoEDebug]:
     """moe_debug of the given device tensors and stage events (None if neither)."""
     if debug is None and events is None:
@@ -257,11 +265,10 @@ class MoELayer:
         if out is not None:
             _check_tensor("out", out, dev, torch.bfloat16, (T, self.d))
         if stats is not None:
-            for name, t, dtype, n in zip(("expert_counts", "dropped", "aux_loss", "z_loss"), stats,
-                                         (torch.int32, torch.int32, torch.float32, torch.float32), (self.E, 1, 1, 1)):
-                _check_tensor(name, t, dev, dtype, (n,))
+            for name, t, n in zip(("expert_counts", "dropped", "aux_loss", "z_loss"), stats, (self.E, 1, 1, 1)):
+                _check_room(name, t, dev, 4 * n)
         if workspace is not None:
-            _check_tensor("workspace", workspace, dev, torch.uint8)
+            _check_room("workspace", workspace, dev, 0)  # (its size is the C entry's to check)
         if debug is not None:
             self._check_debug(debug, T, dev)
         with _on(dev, stream) as handle:
@@ -349,7 +356,8 @@ class MoELayer:
             if name not in form:
                 raise ValueError(f"debug: no field {name}")
             if t is not None:
-                _check_tensor(name, t, index, form[name][1], form[name][0])
+                shape, dtype = form[name]
+                _check_room(name, t, index, math.prod(shape) * dtype.itemsize)
 
     def debug_buffers(self, T: int, device) -> dict:
         """Device tensors for every output field of moe_debug."""

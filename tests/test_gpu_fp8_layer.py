@@ -366,11 +366,11 @@ def test_refusals_of_results_and_workspaces_of_the_wrong_form():
 
     dbg = layer.debug_buffers(w.T, "cuda")
     n = layer.workspace_bytes_fp8(w.T)
-    for kw in (dict(stats=stats(n=w.E - 1)), dict(stats=stats(counts=torch.int64)), dict(stats=stats(losses=torch.float64)),
+    for kw in (dict(stats=stats(n=w.E - 1)), dict(stats=stats(counts=torch.int16)), dict(stats=stats(losses=torch.bfloat16)),
                dict(stats=stats(device="cpu")), dict(workspace=torch.empty(n, dtype=torch.uint8)),
-               dict(workspace=torch.empty(n, dtype=torch.float32, device="cuda")),
                dict(workspace=torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2]),
-               dict(debug=dict(dbg, y_f32=dbg["y_f32"][1:])), dict(debug=dict(dbg, topk_idx=dbg["topk_idx"].long())),
+               dict(debug=dict(dbg, y_f32=dbg["y_f32"][1:])), dict(debug=dict(dbg, topk_idx=dbg["topk_idx"].short())),
+               dict(debug=dict(dbg, y_f32=dbg["y_f32"].t())),
                dict(debug=dict(dbg, lse_out=dbg["lse_out"].cpu())), dict(debug=dict(logits=dbg["logits_out"]))):
         with pytest.raises(ValueError):
             call(**kw)
